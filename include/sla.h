@@ -264,6 +264,129 @@ SLA_API sla_status sla_backward_gated(const sla_shape* shape, const void* q, con
                                       float* dw_proj, float* d_logit, void* workspace,
                                       size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ causal operators
+ *
+ * The causal counterparts of the two branches, over packed sequences of
+ * different lengths: exact softmax attention with grouped heads, and linear
+ * attention with a decay for each head.  They share the conventions above
+ * (device pointers, caller-owned buffers, workspace with an error word,
+ * asynchronous calls) and differ in the layout:
+ *   - q, k, v, o and their gradients are bf16, one row for each token:
+ *     element (row, head, x) is at row * strides.row + head * strides.head + x.
+ *     Strides are in elements, multiples of 8, and no two elements may share a
+ *     place; {0, 0} means contiguous [rows, heads, d].  So slices of a fused
+ *     projection [rows, (Hq + 2 Hkv) d] and head-major tensors [heads, rows, d]
+ *     are passed as they are.  Base addresses are 16-byte aligned.
+ *   - sequence i takes the rows off[i] .. off[i+1]-1 (off: int32 [n_seq + 1] on
+ *     the device).  Empty sequences are allowed.  Rows in no sequence are
+ *     neither read into a result nor written.
+ *   - Offsets are checked on the device: a sequence whose offsets decrease or
+ *     leave the tensor is skipped (nothing of it is written) and the call
+ *     records SLA_ERR_DEVICE in the workspace (sla_check).
+ *   - Results do not depend on the order in which CTAs run: no atomics, equal
+ *     inputs give equal bits.
+ *   - The workspace is taken as with the other calls: 1024-byte aligned,
+ *     sla_workspace_init() once, calls sharing it must not overlap.  It is one
+ *     size for forward and backward. */
+typedef struct {
+  int64_t row, head;
+} sla_strides;
+
+/* Shape of packed causal attention.  Hq is a multiple of Hkv: query head h
+ * reads key/value head h / (Hq / Hkv).  d is 64 or 128.  1 <= total_q, total_k
+ * < 2^30, 1 <= n_seq <= 2^20, Hq <= 1024.
+ * max_q: an upper bound of a sequence's queries, 0 for total_q.  It only picks
+ * the kernel; a longer sequence is skipped and reported like a bad offset.
+ * softmax_scale <= 0 selects 1/sqrt(d). */
+typedef struct {
+  int n_seq, total_q, total_k, Hq, Hkv, d;
+  int max_q;
+  float softmax_scale;
+  sla_strides q, k, v, o;
+} sla_causal_shape;
+
+/* Sizes in bytes for a causal shape. */
+typedef struct {
+  size_t lse_bytes, workspace_bytes;
+} sla_causal_sizes;
+
+/* Host only; no CUDA call. */
+SLA_API sla_status sla_causal_query_sizes(const sla_causal_shape* shape, sla_causal_sizes* out);
+
+/* Causal attention of packed sequences.  Sequence i has the queries
+ * q_off[i] .. q_off[i+1]-1 (Lq of them) and the keys k_off[i] .. k_off[i]+Lk-1,
+ * Lk = k_len[i], or k_off[i+1]-k_off[i] where k_len is NULL (with k_len, which
+ * suits caches of a fixed capacity, only k_off[0..n_seq-1] are read, in any
+ * order, and sequences may share keys).  Query a sees the keys
+ * b <= a + Lk - Lq, so that the last query sees every key:
+ *   s_ab = softmax_scale q_a . k_b,  lse_a = log sum_b exp s_ab,
+ *   o_a  = sum_b exp(s_ab - lse_a) v_b.
+ * A query that sees no key (Lk - Lq + a < 0) gets o = 0, lse = -inf.
+ * Lq = Lk is a whole prompt, Lq < Lk a prompt that continues, Lq = 1 a
+ * generated token.  o: bf16; lse: fp32 [Hq, total_q].  The contents of keys and
+ * values outside a sequence's Lk do not matter (they may be NaN); within a
+ * sequence a key's value may reach earlier queries if it is not finite. */
+SLA_API sla_status sla_causal_forward(const sla_causal_shape* shape, const void* q, const void* k,
+                                      const void* v, const int32_t* q_off, const int32_t* k_off,
+                                      const int32_t* k_len, void* o, float* lse, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(o * d_o) for the forward above without k_len.  o and lse are
+ * the forward's; d_o has o's strides; dq, dk, dv (bf16) have those of q, k, v
+ * and are overwritten at every row of a sequence (0 where nothing is seen). */
+SLA_API sla_status sla_causal_backward(const sla_causal_shape* shape, const void* q, const void* k,
+                                       const void* v, const int32_t* q_off, const int32_t* k_off,
+                                       const void* o, const float* lse, const void* d_o, void* dq,
+                                       void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* Shape of the decayed linear attention: every head has its own q, k, v.
+ * Limits as for sla_causal_shape.  scale <= 0 selects 1/sqrt(d). */
+typedef struct {
+  int n_seq, total, H, d;
+  float scale;
+  sla_strides q, k, v, o;
+} sla_decay_shape;
+
+typedef struct {
+  size_t state_bytes, workspace_bytes;
+} sla_decay_sizes;
+
+/* Host only; no CUDA call. */
+SLA_API sla_status sla_decay_query_sizes(const sla_decay_shape* shape, sla_decay_sizes* out);
+
+/* Linear attention with a decay for each head: with l = exp(log_decay[h]),
+ *   S_t = l S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,
+ * S_{-1} = state_in[i] (0 where state_in is NULL), state_out[i] = S of the last
+ * token (NULL: not written).  States: fp32 [n_seq, H, d (of k), d (of v)],
+ * 16-byte aligned; state_in and state_out may be the same buffer.  An empty
+ * sequence passes its state on.  log_decay: fp32 [H] on the device, at most 0
+ * (-inf forgets at once); a value above 0 or NaN is taken as 0 and reported as
+ * SLA_ERR_DEVICE. */
+SLA_API sla_status sla_decay_forward(const sla_decay_shape* shape, const void* q, const void* k,
+                                     const void* v, const float* log_decay, const int32_t* off,
+                                     const float* state_in, void* o, float* state_out,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(o * d_o) + sum(state_out * d_state_out), the decays held
+ * fixed.  d_state_out may be NULL (0); d_o has o's strides; dq, dk, dv (bf16)
+ * those of q, k, v; d_state_in (fp32, the state's layout, may be the same
+ * buffer as d_state_out) may be NULL. */
+SLA_API sla_status sla_decay_backward(const sla_decay_shape* shape, const void* q, const void* k,
+                                      const void* v, const float* log_decay, const int32_t* off,
+                                      const float* state_in, const void* d_o,
+                                      const float* d_state_out, void* dq, void* dk, void* dv,
+                                      float* d_state_in, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/* One token for each sequence (total = n_seq, row i belongs to sequence i):
+ * S = l state_in + k v^T, o = scale S^T q, state_out = S; both states are
+ * required and may be the same buffer.  A log_decay above 0 or NaN is taken as
+ * 0.  Takes no workspace. */
+SLA_API sla_status sla_decay_step(const sla_decay_shape* shape, const void* q, const void* k,
+                                  const void* v, const float* log_decay, const float* state_in,
+                                  float* state_out, void* o, void* stream);
+
 /* Zero the workspace's device error word (asynchronously on `stream`).  Call
  * once on a new workspace before its first use; sla_check() clears it
  * afterwards. */

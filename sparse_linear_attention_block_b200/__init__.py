@@ -9,7 +9,8 @@ The entry points mirror the C names (``sla_query_sizes``, ``sla_classify``,
 ``sla_classify_from_scores``, ``sla_forward``, ``sla_backward``,
 ``sla_workspace_init``, ``sla_check``, ``sla_strerror``, ``sla_version``) and
 take torch tensors where the C ABI takes device pointers.  ``Buffers`` allocates
-every caller-owned buffer for a shape with torch.
+every caller-owned buffer for a shape with torch.  The causal operators
+(``sla_causal_*``, ``sla_decay_*``) are in :mod:`.causal` and exported here.
 """
 
 from __future__ import annotations
@@ -25,7 +26,10 @@ __all__ = [
     "sla_profile_begin", "sla_profile_end", "KernelStat", "make_shape", "EXPORTED_SYMBOLS",
     "STATUS", "Gate", "sla_forward_gated", "sla_backward_gated", "Hierarchy",
     "sla_hierarchy_counts", "sla_classify_hierarchical", "sla_classify_hierarchical_from_scores",
-    "sla_debug_inject", "INJECT_WITHHOLD_LOADS",
+    "sla_debug_inject", "INJECT_WITHHOLD_LOADS", "Strides", "CausalShape", "CausalSizes",
+    "DecayShape", "DecaySizes", "CausalBuffers", "DecayBuffers", "make_causal_shape",
+    "make_decay_shape", "sla_causal_query_sizes", "sla_causal_forward", "sla_causal_backward",
+    "sla_decay_query_sizes", "sla_decay_forward", "sla_decay_backward", "sla_decay_step",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -39,7 +43,10 @@ EXPORTED_SYMBOLS = ["sla_query_sizes", "sla_classify", "sla_classify_from_scores
                     "sla_strerror", "sla_version", "sla_profile_begin", "sla_profile_end",
                     "sla_classify_noalloc", "sla_forward_gated", "sla_backward_gated",
                     "sla_hierarchy_counts", "sla_classify_hierarchical",
-                    "sla_classify_hierarchical_from_scores", "sla_debug_inject"]
+                    "sla_classify_hierarchical_from_scores", "sla_debug_inject",
+                    "sla_causal_query_sizes", "sla_causal_forward", "sla_causal_backward",
+                    "sla_decay_query_sizes", "sla_decay_forward", "sla_decay_backward",
+                    "sla_decay_step"]
 
 INJECT_WITHHOLD_LOADS = 1  # SLA_INJECT_WITHHOLD_LOADS of sla.h
 
@@ -139,6 +146,7 @@ def lib() -> ctypes.CDLL:
                   "sla_hierarchy_counts", "sla_classify_hierarchical",
                   "sla_classify_hierarchical_from_scores", "sla_debug_inject"):
             getattr(L, n).restype = st
+        causal.declare(L)
         _lib = L
     return _lib
 
@@ -357,3 +365,11 @@ class Buffers:
         b.saved = SavedStruct(_ptr(b.lse), _ptr(b.o_s), _ptr(b.den), _ptr(b.hz_agg))
         sla_workspace_init(b.workspace, stream)
         return b
+
+
+from . import causal  # noqa: E402  (uses the helpers above)
+from .causal import (  # noqa: E402
+    CausalBuffers, CausalShape, CausalSizes, DecayBuffers, DecayShape, DecaySizes, Strides,
+    make_causal_shape, make_decay_shape, sla_causal_backward, sla_causal_forward,
+    sla_causal_query_sizes, sla_decay_backward, sla_decay_forward, sla_decay_query_sizes,
+    sla_decay_step)

@@ -1,0 +1,103 @@
+// Internal declarations of the causal operators (packed softmax attention with
+// grouped heads, linear attention with per-head decay).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+#include "sla_internal.h"
+
+namespace sla {
+
+// A bf16 tensor of rows x heads x d, strides in elements.
+struct RowView {
+  const __nv_bfloat16* p;
+  long long row, head;
+};
+struct RowOut {
+  __nv_bfloat16* p;
+  long long row, head;
+};
+
+// A sequence after the device-side check: first query row and count, first key
+// row and count (counts 0 where the offsets were bad).
+struct Seq {
+  int q0, nq, k0, nk;
+};
+
+struct CausalProblem {
+  int n_seq, total_q, total_k, Hq, Hkv, G, d, max_q;
+  float scale, scale_log2;
+  sla_strides q, k, v, o;  // resolved
+};
+
+struct CausalLayout {
+  size_t err;    // the 256-byte header
+  size_t seqs;   // Seq [n_seq]
+  size_t dvec;   // fp32 [Hq, total_q]: D_a = o_a . do_a
+  size_t total;
+};
+
+struct DecayProblem {
+  int n_seq, total, H, d;
+  float scale;
+  sla_strides q, k, v, o;
+};
+
+struct DecayLayout {
+  size_t err;
+  size_t seqs;  // Seq [n_seq] (k0, nk unused)
+  size_t total;
+};
+
+cudaError_t launch_causal_plan(const CausalProblem& p, const int32_t* q_off, const int32_t* k_off,
+                               const int32_t* k_len, Seq* seqs, int* err, cudaStream_t s);
+cudaError_t launch_causal_fwd(const CausalProblem& p, const void* q, const void* k, const void* v,
+                              const Seq* seqs, void* o, float* lse, int* err, cudaStream_t s);
+cudaError_t launch_causal_dvec(const CausalProblem& p, const Seq* seqs, const void* o,
+                               const void* d_o, float* dvec, cudaStream_t s);
+cudaError_t launch_causal_dq(const CausalProblem& p, const void* q, const void* k, const void* v,
+                             const Seq* seqs, const void* d_o, const float* lse, const float* dvec,
+                             void* dq, int* err, cudaStream_t s);
+cudaError_t launch_causal_dkv(const CausalProblem& p, const void* q, const void* k, const void* v,
+                              const Seq* seqs, const void* d_o, const float* lse,
+                              const float* dvec, void* dk, void* dv, int* err, cudaStream_t s);
+
+// One recurrence R over a sequence's tokens, in order or from the last to the
+// first, and what is read from it:
+//   forward:  R = l R + y_t z_t^T,        out_t = fs_out R^T x_t
+//   reverse:  R = R + fs_up y_t z_t^T,    out_t = R^T x_t,   then R = l R
+// (R is [d of y][d of z]).  state_in / state_out: R before the first and after
+// the last step, stored [z][y] where `state_t`.
+struct DecayRun {
+  RowView x, y, z;
+  RowOut out;
+  const float* state_in;
+  float* state_out;
+  bool reverse, state_t;
+};
+cudaError_t launch_decay_plan(const DecayProblem& p, const int32_t* off, const float* log_decay,
+                              Seq* seqs, int* err, cudaStream_t s);
+cudaError_t launch_decay_run(const DecayProblem& p, const DecayRun& r, const Seq* seqs,
+                             const float* log_decay, int* err, cudaStream_t s);
+cudaError_t launch_decay_step(const DecayProblem& p, const void* q, const void* k, const void* v,
+                              const float* log_decay, const float* state_in, float* state_out,
+                              void* o, cudaStream_t s);
+
+// exp(n g) for a checked log-decay g <= 0 (1 at n = 0, also where g is -inf), as a sum of
+// two fp32 numbers.  A factor that is applied again and again to a state has to be exact
+// beyond fp32: rounded to one number, a decay of nearly 1 drifts by 2^-24 each time.
+struct Factor {
+  float hi, lo;
+};
+__device__ __forceinline__ Factor decay_factor(float g, int n) {
+  const double x = n == 0 ? 1.0 : exp(double(g) * n);
+  const float hi = float(x);
+  return {hi, float(x - hi)};
+}
+__device__ __forceinline__ float scaled(float s, const Factor& f) { return fmaf(s, f.hi, s * f.lo); }
+__device__ __forceinline__ float decay_checked(float g) { return g <= 0.f ? g : 0.f; }
+
+}  // namespace sla

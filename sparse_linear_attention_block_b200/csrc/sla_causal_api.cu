@@ -1,0 +1,269 @@
+// C-ABI entry points of the causal operators: argument validation, workspace
+// layout and the launch sequence of each call.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "sla.h"
+#include "sla_causal.h"
+
+using namespace sla;
+
+namespace {
+
+constexpr int kMaxRows = 1 << 30, kMaxSeqs = 1 << 20, kMaxHeads = 1024;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// a required 16-byte aligned pointer
+bool good(const void* p) { return p && aligned(p, 16); }
+// an optional one
+bool good_or_null(const void* p) { return aligned(p, 16); }
+
+// Strides of a [rows, heads, d] tensor: resolves {0, 0} and refuses strides
+// that are not multiples of 8 elements or let two elements share a place.
+bool resolve(sla_strides in, long long rows, long long heads, int d, sla_strides* out) {
+  if (in.row == 0 && in.head == 0) in = sla_strides{heads * d, d};
+  if (in.row < d || in.head < d || in.row % 8 || in.head % 8) return false;
+  const long long most = 1ll << 37;  // 2^38 bytes, the range of a tensor map's stride
+  if (in.row >= most || in.head >= most) return false;
+  const bool rows_outer = in.row >= (heads - 1) * in.head + d || rows == 1;
+  const bool heads_outer = in.head >= (rows - 1) * in.row + d || heads == 1;
+  if (!rows_outer && !heads_outer) return false;
+  *out = in;
+  return true;
+}
+
+bool good_scale(float f) { return std::isfinite(f); }
+
+sla_status check_causal(const sla_causal_shape* s, CausalProblem* p) {
+  if (!s) return SLA_ERR_INVALID_ARG;
+  if (s->n_seq < 1 || s->total_q < 1 || s->total_k < 1 || s->Hq < 1 || s->Hkv < 1 || s->d < 1 ||
+      s->max_q < 0 || s->Hq % s->Hkv != 0 || !good_scale(s->softmax_scale))
+    return SLA_ERR_INVALID_ARG;
+  if ((s->d != 64 && s->d != 128) || s->n_seq > kMaxSeqs || s->total_q >= kMaxRows ||
+      s->total_k >= kMaxRows || s->Hq > kMaxHeads)
+    return SLA_ERR_UNSUPPORTED;
+  p->n_seq = s->n_seq;
+  p->total_q = s->total_q;
+  p->total_k = s->total_k;
+  p->Hq = s->Hq;
+  p->Hkv = s->Hkv;
+  p->G = s->Hq / s->Hkv;
+  p->d = s->d;
+  p->max_q = s->max_q > 0 && s->max_q < s->total_q ? s->max_q : s->total_q;
+  p->scale = s->softmax_scale > 0.f ? s->softmax_scale : 1.0f / std::sqrt(float(s->d));
+  p->scale_log2 = p->scale * 1.4426950408889634f;
+  if (!resolve(s->q, s->total_q, s->Hq, s->d, &p->q) ||
+      !resolve(s->k, s->total_k, s->Hkv, s->d, &p->k) ||
+      !resolve(s->v, s->total_k, s->Hkv, s->d, &p->v) ||
+      !resolve(s->o, s->total_q, s->Hq, s->d, &p->o))
+    return SLA_ERR_INVALID_ARG;
+  return SLA_OK;
+}
+
+sla_status check_decay(const sla_decay_shape* s, DecayProblem* p) {
+  if (!s) return SLA_ERR_INVALID_ARG;
+  if (s->n_seq < 1 || s->total < 1 || s->H < 1 || s->d < 1 || !good_scale(s->scale))
+    return SLA_ERR_INVALID_ARG;
+  if ((s->d != 64 && s->d != 128) || s->n_seq > kMaxSeqs || s->total >= kMaxRows ||
+      s->H > kMaxHeads)
+    return SLA_ERR_UNSUPPORTED;
+  p->n_seq = s->n_seq;
+  p->total = s->total;
+  p->H = s->H;
+  p->d = s->d;
+  p->scale = s->scale > 0.f ? s->scale : 1.0f / std::sqrt(float(s->d));
+  if (!resolve(s->q, s->total, s->H, s->d, &p->q) || !resolve(s->k, s->total, s->H, s->d, &p->k) ||
+      !resolve(s->v, s->total, s->H, s->d, &p->v) || !resolve(s->o, s->total, s->H, s->d, &p->o))
+    return SLA_ERR_INVALID_ARG;
+  return SLA_OK;
+}
+
+struct Taker {
+  size_t off = 0;
+  size_t operator()(size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, kAlign);
+    return at;
+  }
+};
+
+CausalLayout causal_layout(const CausalProblem& p) {
+  Taker take;
+  CausalLayout L{};
+  L.err = take(256);
+  L.seqs = take(size_t(p.n_seq) * sizeof(Seq));
+  L.dvec = take(size_t(p.Hq) * p.total_q * 4);
+  L.total = take.off;
+  return L;
+}
+
+DecayLayout decay_layout(const DecayProblem& p) {
+  Taker take;
+  DecayLayout L{};
+  L.err = take(256);
+  L.seqs = take(size_t(p.n_seq) * sizeof(Seq));
+  L.total = take.off;
+  return L;
+}
+
+sla_status check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (!ws || !aligned(ws, kAlign)) return SLA_ERR_INVALID_ARG;
+  return bytes < need ? SLA_ERR_WORKSPACE : SLA_OK;
+}
+
+template <typename T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
+}
+
+RowView view(const void* p, const sla_strides& s) {
+  return {static_cast<const __nv_bfloat16*>(p), s.row, s.head};
+}
+RowOut out_view(void* p, const sla_strides& s) {
+  return {static_cast<__nv_bfloat16*>(p), s.row, s.head};
+}
+
+#define SLA_LAUNCH(name, stream, expr)                                     \
+  do {                                                                     \
+    if (launch_named(name, stream, [&] { return (expr); }) != cudaSuccess) \
+      return SLA_ERR_CUDA;                                                 \
+  } while (0)
+
+}  // namespace
+
+extern "C" {
+
+sla_status sla_causal_query_sizes(const sla_causal_shape* shape, sla_causal_sizes* out) {
+  if (!out) return SLA_ERR_INVALID_ARG;
+  CausalProblem p;
+  const sla_status st = check_causal(shape, &p);
+  if (st != SLA_OK) return st;
+  out->lse_bytes = size_t(p.Hq) * p.total_q * 4;
+  out->workspace_bytes = causal_layout(p).total;
+  return SLA_OK;
+}
+
+sla_status sla_causal_forward(const sla_causal_shape* shape, const void* q, const void* k,
+                              const void* v, const int32_t* q_off, const int32_t* k_off,
+                              const int32_t* k_len, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  CausalProblem p;
+  sla_status st = check_causal(shape, &p);
+  if (st != SLA_OK) return st;
+  if (!good(q) || !good(k) || !good(v) || !good(o) || !lse || !aligned(lse, 4) || !q_off ||
+      !k_off || !aligned(q_off, 4) || !aligned(k_off, 4) || !aligned(k_len, 4))
+    return SLA_ERR_INVALID_ARG;
+  const CausalLayout L = causal_layout(p);
+  if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* err = at<int>(workspace, L.err);
+  Seq* seqs = at<Seq>(workspace, L.seqs);
+  SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, k_len, seqs, err, s));
+  SLA_LAUNCH("causal_fwd", s, launch_causal_fwd(p, q, k, v, seqs, o, lse, err, s));
+  return SLA_OK;
+}
+
+sla_status sla_causal_backward(const sla_causal_shape* shape, const void* q, const void* k,
+                               const void* v, const int32_t* q_off, const int32_t* k_off,
+                               const void* o, const float* lse, const void* d_o, void* dq, void* dk,
+                               void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  CausalProblem p;
+  sla_status st = check_causal(shape, &p);
+  if (st != SLA_OK) return st;
+  if (!good(q) || !good(k) || !good(v) || !good(o) || !good(d_o) || !good(dq) || !good(dk) ||
+      !good(dv) || !lse || !aligned(lse, 4) || !q_off || !k_off || !aligned(q_off, 4) ||
+      !aligned(k_off, 4))
+    return SLA_ERR_INVALID_ARG;
+  const CausalLayout L = causal_layout(p);
+  if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* err = at<int>(workspace, L.err);
+  Seq* seqs = at<Seq>(workspace, L.seqs);
+  float* dvec = at<float>(workspace, L.dvec);
+  SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, nullptr, seqs, err, s));
+  SLA_LAUNCH("causal_dvec", s, launch_causal_dvec(p, seqs, o, d_o, dvec, s));
+  SLA_LAUNCH("causal_dkv", s,
+             launch_causal_dkv(p, q, k, v, seqs, d_o, lse, dvec, dk, dv, err, s));
+  SLA_LAUNCH("causal_dq", s, launch_causal_dq(p, q, k, v, seqs, d_o, lse, dvec, dq, err, s));
+  return SLA_OK;
+}
+
+sla_status sla_decay_query_sizes(const sla_decay_shape* shape, sla_decay_sizes* out) {
+  if (!out) return SLA_ERR_INVALID_ARG;
+  DecayProblem p;
+  const sla_status st = check_decay(shape, &p);
+  if (st != SLA_OK) return st;
+  out->state_bytes = size_t(p.n_seq) * p.H * p.d * p.d * 4;
+  out->workspace_bytes = decay_layout(p).total;
+  return SLA_OK;
+}
+
+sla_status sla_decay_forward(const sla_decay_shape* shape, const void* q, const void* k,
+                             const void* v, const float* log_decay, const int32_t* off,
+                             const float* state_in, void* o, float* state_out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  DecayProblem p;
+  sla_status st = check_decay(shape, &p);
+  if (st != SLA_OK) return st;
+  if (!good(q) || !good(k) || !good(v) || !good(o) || !log_decay || !aligned(log_decay, 4) ||
+      !off || !aligned(off, 4) || !good_or_null(state_in) || !good_or_null(state_out))
+    return SLA_ERR_INVALID_ARG;
+  const DecayLayout L = decay_layout(p);
+  if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* err = at<int>(workspace, L.err);
+  Seq* seqs = at<Seq>(workspace, L.seqs);
+  SLA_LAUNCH("decay_plan", s, launch_decay_plan(p, off, log_decay, seqs, err, s));
+  const DecayRun r{view(q, p.q), view(k, p.k), view(v, p.v), out_view(o, p.o),
+                   state_in,     state_out,    false,        false};
+  SLA_LAUNCH("decay_fwd", s, launch_decay_run(p, r, seqs, log_decay, err, s));
+  return SLA_OK;
+}
+
+sla_status sla_decay_backward(const sla_decay_shape* shape, const void* q, const void* k,
+                              const void* v, const float* log_decay, const int32_t* off,
+                              const float* state_in, const void* d_o, const float* d_state_out,
+                              void* dq, void* dk, void* dv, float* d_state_in, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  DecayProblem p;
+  sla_status st = check_decay(shape, &p);
+  if (st != SLA_OK) return st;
+  if (!good(q) || !good(k) || !good(v) || !good(d_o) || !good(dq) || !good(dk) || !good(dv) ||
+      !log_decay || !aligned(log_decay, 4) || !off || !aligned(off, 4) ||
+      !good_or_null(state_in) || !good_or_null(d_state_out) || !good_or_null(d_state_in))
+    return SLA_ERR_INVALID_ARG;
+  const DecayLayout L = decay_layout(p);
+  if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* err = at<int>(workspace, L.err);
+  Seq* seqs = at<Seq>(workspace, L.seqs);
+  SLA_LAUNCH("decay_plan", s, launch_decay_plan(p, off, log_decay, seqs, err, s));
+  const RowView vq = view(q, p.q), vk = view(k, p.k), vv = view(v, p.v), vd = view(d_o, p.o);
+  const DecayRun rq{vd, vv, vk, out_view(dq, p.q), state_in, nullptr, false, true};
+  const DecayRun rk{vv, vd, vq, out_view(dk, p.k), d_state_out, nullptr, true, true};
+  // last: d_state_in may be d_state_out's buffer
+  const DecayRun rv{vk, vq, vd, out_view(dv, p.v), d_state_out, d_state_in, true, false};
+  SLA_LAUNCH("decay_dq", s, launch_decay_run(p, rq, seqs, log_decay, err, s));
+  SLA_LAUNCH("decay_dk", s, launch_decay_run(p, rk, seqs, log_decay, err, s));
+  SLA_LAUNCH("decay_dv", s, launch_decay_run(p, rv, seqs, log_decay, err, s));
+  return SLA_OK;
+}
+
+sla_status sla_decay_step(const sla_decay_shape* shape, const void* q, const void* k,
+                          const void* v, const float* log_decay, const float* state_in,
+                          float* state_out, void* o, void* stream) {
+  DecayProblem p;
+  const sla_status st = check_decay(shape, &p);
+  if (st != SLA_OK) return st;
+  if (p.total != p.n_seq || !good(q) || !good(k) || !good(v) || !good(o) || !log_decay ||
+      !aligned(log_decay, 4) || !good(state_in) || !good(state_out))
+    return SLA_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  SLA_LAUNCH("decay_step", s,
+             launch_decay_step(p, q, k, v, log_decay, state_in, state_out, o, s));
+  return SLA_OK;
+}
+
+}  // extern "C"

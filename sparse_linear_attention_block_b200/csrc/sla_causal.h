@@ -27,16 +27,38 @@ struct Seq {
   int q0, nq, k0, nk;
 };
 
+// One tile of a causal kernel's work list: tile number `tile` of sequence `seq`.
+struct alignas(16) Item {
+  Seq s;
+  int tile, seq, pad0, pad1;
+};
+// A work list: its items in order of falling cost, and how many there are.
+struct ItemList {
+  const int* count;
+  const Item* items;
+  int most;  // the list has room for that many
+};
+
 struct CausalProblem {
   int n_seq, total_q, total_k, Hq, Hkv, G, d, max_q;
   float scale, scale_log2;
   sla_strides q, k, v, o;  // resolved
 };
 
+// Tile heights of the work lists: queries of a forward CTA (one head's two
+// tiles of 128, or one tile of 128 for two heads that share their keys),
+// queries of a dQ CTA, keys of a dK/dV CTA.
+constexpr int kRowTile = 128;
+inline bool pair_heads(const CausalProblem& p) { return p.G % 2 == 0; }
+inline int fwd_tile(const CausalProblem& p) { return pair_heads(p) ? kRowTile : 2 * kRowTile; }
+inline size_t most_items(int rows, int tile, int n_seq) { return size_t(rows / tile) + n_seq; }
+
 struct CausalLayout {
-  size_t err;    // the 256-byte header
-  size_t seqs;   // Seq [n_seq]
-  size_t dvec;   // fp32 [Hq, total_q]: D_a = o_a . do_a
+  size_t err;     // the 256-byte header
+  size_t counts;  // int [2]: items of each list
+  size_t items;   // Item [..]: the forward's list, or the dQ list
+  size_t kitems;  // Item [..]: the dK/dV list
+  size_t dvec;    // fp32 [Hq, total_q]: D_a = o_a . do_a
   size_t total;
 };
 
@@ -52,18 +74,35 @@ struct DecayLayout {
   size_t total;
 };
 
+// What a plan makes: the list of query tiles and, for a backward, of key tiles.
+struct CausalPlan {
+  int q_tile;
+  Item* q_items;
+  int* q_count;
+  Item* k_items;  // may be null
+  int* k_count;
+};
 cudaError_t launch_causal_plan(const CausalProblem& p, const int32_t* q_off, const int32_t* k_off,
-                               const int32_t* k_len, Seq* seqs, int* err, cudaStream_t s);
+                               const int32_t* k_len, const CausalPlan& plan, int* err,
+                               cudaStream_t s);
 cudaError_t launch_causal_fwd(const CausalProblem& p, const void* q, const void* k, const void* v,
-                              const Seq* seqs, void* o, float* lse, int* err, cudaStream_t s);
-cudaError_t launch_causal_dvec(const CausalProblem& p, const Seq* seqs, const void* o,
+                              const ItemList& list, void* o, float* lse, int* err, cudaStream_t s);
+cudaError_t launch_causal_dvec(const CausalProblem& p, const ItemList& list, const void* o,
                                const void* d_o, float* dvec, cudaStream_t s);
 cudaError_t launch_causal_dq(const CausalProblem& p, const void* q, const void* k, const void* v,
-                             const Seq* seqs, const void* d_o, const float* lse, const float* dvec,
-                             void* dq, int* err, cudaStream_t s);
+                             const ItemList& list, const void* d_o, const float* lse,
+                             const float* dvec, void* dq, int* err, cudaStream_t s);
 cudaError_t launch_causal_dkv(const CausalProblem& p, const void* q, const void* k, const void* v,
-                              const Seq* seqs, const void* d_o, const float* lse,
+                              const ItemList& list, const void* d_o, const float* lse,
                               const float* dvec, void* dk, void* dv, int* err, cudaStream_t s);
+
+// TMA descriptor of a bf16 [rows, heads, d] tensor with the given strides: coordinates
+// (feature, row, head), boxes of 64 features x box_rows rows of one head, 128-byte swizzle.
+inline bool make_tmap_rows(CUtensorMap* m, const void* base, int rows, int heads, int d,
+                           const sla_strides& st, int box_rows) {
+  return make_tmap_strided(m, base, uint64_t(d), uint64_t(rows), uint64_t(heads),
+                           uint64_t(st.row), uint64_t(st.head), 64, uint32_t(box_rows));
+}
 
 // One recurrence R over a sequence's tokens, in order or from the last to the
 // first, and what is read from it:
@@ -99,5 +138,13 @@ __device__ __forceinline__ Factor decay_factor(float g, int n) {
 }
 __device__ __forceinline__ float scaled(float s, const Factor& f) { return fmaf(s, f.hi, s * f.lo); }
 __device__ __forceinline__ float decay_checked(float g) { return g <= 0.f ? g : 0.f; }
+
+// Write 8 consecutive 32-bit TMEM columns of a warp's 32 lanes.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
 
 }  // namespace sla

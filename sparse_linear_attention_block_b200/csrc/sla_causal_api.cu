@@ -59,6 +59,10 @@ sla_status check_causal(const sla_causal_shape* s, CausalProblem* p) {
       !resolve(s->v, s->total_k, s->Hkv, s->d, &p->v) ||
       !resolve(s->o, s->total_q, s->Hq, s->d, &p->o))
     return SLA_ERR_INVALID_ARG;
+  // grids: one CTA for each tile and head
+  const size_t tiles = most_items(s->total_q > s->total_k ? s->total_q : s->total_k, kRowTile,
+                                  s->n_seq);
+  if (tiles * size_t(s->Hq) >= (1u << 31)) return SLA_ERR_UNSUPPORTED;
   return SLA_OK;
 }
 
@@ -93,7 +97,9 @@ CausalLayout causal_layout(const CausalProblem& p) {
   Taker take;
   CausalLayout L{};
   L.err = take(256);
-  L.seqs = take(size_t(p.n_seq) * sizeof(Seq));
+  L.counts = take(2 * sizeof(int));
+  L.items = take(most_items(p.total_q, kRowTile, p.n_seq) * sizeof(Item));
+  L.kitems = take(most_items(p.total_k, kRowTile, p.n_seq) * sizeof(Item));
   L.dvec = take(size_t(p.Hq) * p.total_q * 4);
   L.total = take.off;
   return L;
@@ -159,9 +165,12 @@ sla_status sla_causal_forward(const sla_causal_shape* shape, const void* q, cons
   if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = at<int>(workspace, L.err);
-  Seq* seqs = at<Seq>(workspace, L.seqs);
-  SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, k_len, seqs, err, s));
-  SLA_LAUNCH("causal_fwd", s, launch_causal_fwd(p, q, k, v, seqs, o, lse, err, s));
+  int* counts = at<int>(workspace, L.counts);
+  Item* items = at<Item>(workspace, L.items);
+  const CausalPlan plan{fwd_tile(p), items, counts, nullptr, nullptr};
+  SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, k_len, plan, err, s));
+  const ItemList list{counts, items, int(most_items(p.total_q, plan.q_tile, p.n_seq))};
+  SLA_LAUNCH("causal_fwd", s, launch_causal_fwd(p, q, k, v, list, o, lse, err, s));
   return SLA_OK;
 }
 
@@ -180,13 +189,17 @@ sla_status sla_causal_backward(const sla_causal_shape* shape, const void* q, con
   if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = at<int>(workspace, L.err);
-  Seq* seqs = at<Seq>(workspace, L.seqs);
+  int* counts = at<int>(workspace, L.counts);
+  Item *items = at<Item>(workspace, L.items), *kitems = at<Item>(workspace, L.kitems);
   float* dvec = at<float>(workspace, L.dvec);
-  SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, nullptr, seqs, err, s));
-  SLA_LAUNCH("causal_dvec", s, launch_causal_dvec(p, seqs, o, d_o, dvec, s));
+  const CausalPlan plan{kRowTile, items, counts, kitems, counts + 1};
+  SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, nullptr, plan, err, s));
+  const ItemList list{counts, items, int(most_items(p.total_q, kRowTile, p.n_seq))};
+  const ItemList klist{counts + 1, kitems, int(most_items(p.total_k, kRowTile, p.n_seq))};
+  SLA_LAUNCH("causal_dvec", s, launch_causal_dvec(p, list, o, d_o, dvec, s));
   SLA_LAUNCH("causal_dkv", s,
-             launch_causal_dkv(p, q, k, v, seqs, d_o, lse, dvec, dk, dv, err, s));
-  SLA_LAUNCH("causal_dq", s, launch_causal_dq(p, q, k, v, seqs, d_o, lse, dvec, dq, err, s));
+             launch_causal_dkv(p, q, k, v, klist, d_o, lse, dvec, dk, dv, err, s));
+  SLA_LAUNCH("causal_dq", s, launch_causal_dq(p, q, k, v, list, d_o, lse, dvec, dq, err, s));
   return SLA_OK;
 }
 

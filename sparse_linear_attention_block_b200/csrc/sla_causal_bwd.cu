@@ -43,12 +43,14 @@ __device__ __forceinline__ float dot(const float (&x)[E], const float (&y)[E]) {
 
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) causal_dvec_kernel(RowView o, RowView d_o,
-                                                                  const Seq* __restrict__ seqs,
+                                                                  const int* __restrict__ count, const Item* __restrict__ items,
                                                                   float* __restrict__ dvec,
                                                                   int total_q) {
-  const Seq sq = seqs[blockIdx.x];
+  if (int(blockIdx.x) >= *count) return;
+  const Seq sq = items[blockIdx.x].s;
+  const int t0 = items[blockIdx.x].tile * kRowTile;
   const int h = blockIdx.y;
-  for (int a = blockIdx.z * kWarps + threadIdx.x / 32; a < sq.nq; a += gridDim.z * kWarps) {
+  for (int a = t0 + threadIdx.x / 32; a < min(sq.nq, t0 + kRowTile); a += kWarps) {
     float x[D / 32], y[D / 32];
     load_row(x, o, size_t(sq.q0) + a, h);
     load_row(y, d_o, size_t(sq.q0) + a, h);
@@ -59,13 +61,15 @@ __global__ void __launch_bounds__(kWarps * 32) causal_dvec_kernel(RowView o, Row
 
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) causal_dq_kernel(
-    RowView q, RowView k, RowView v, RowView d_o, const Seq* __restrict__ seqs,
+    RowView q, RowView k, RowView v, RowView d_o, const int* __restrict__ count, const Item* __restrict__ items,
     const float* __restrict__ lse, const float* __restrict__ dvec, RowOut dq, int total_q, int G,
     float scale) {
   constexpr int E = D / 32;
-  const Seq sq = seqs[blockIdx.x];
+  if (int(blockIdx.x) >= *count) return;
+  const Seq sq = items[blockIdx.x].s;
+  const int t0 = items[blockIdx.x].tile * kRowTile;
   const int h = blockIdx.y;
-  for (int a = blockIdx.z * kWarps + threadIdx.x / 32; a < sq.nq; a += gridDim.z * kWarps) {
+  for (int a = t0 + threadIdx.x / 32; a < min(sq.nq, t0 + kRowTile); a += kWarps) {
     const size_t row = size_t(sq.q0) + a;
     float x[E], g[E], acc[E] = {};
     load_row(x, q, row, h);
@@ -86,13 +90,15 @@ __global__ void __launch_bounds__(kWarps * 32) causal_dq_kernel(
 
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) causal_dkv_kernel(
-    RowView q, RowView k, RowView v, RowView d_o, const Seq* __restrict__ seqs,
+    RowView q, RowView k, RowView v, RowView d_o, const int* __restrict__ count, const Item* __restrict__ items,
     const float* __restrict__ lse, const float* __restrict__ dvec, RowOut dk, RowOut dv,
     int total_q, int G, float scale) {
   constexpr int E = D / 32;
-  const Seq sq = seqs[blockIdx.x];
+  if (int(blockIdx.x) >= *count) return;
+  const Seq sq = items[blockIdx.x].s;
+  const int t0 = items[blockIdx.x].tile * kRowTile;
   const int hk = blockIdx.y;
-  for (int b = blockIdx.z * kWarps + threadIdx.x / 32; b < sq.nk; b += gridDim.z * kWarps) {
+  for (int b = t0 + threadIdx.x / 32; b < min(sq.nk, t0 + kRowTile); b += kWarps) {
     float kk[E], vv[E], ak[E] = {}, av[E] = {};
     load_row(kk, k, size_t(sq.k0) + b, hk);
     load_row(vv, v, size_t(sq.k0) + b, hk);
@@ -122,46 +128,46 @@ RowOut out(void* p, const sla_strides& s) { return {static_cast<__nv_bfloat16*>(
 
 }  // namespace
 
-cudaError_t launch_causal_dvec(const CausalProblem& p, const Seq* seqs, const void* o,
+cudaError_t launch_causal_dvec(const CausalProblem& p, const ItemList& list, const void* o,
                                const void* d_o, float* dvec, cudaStream_t s) {
-  const dim3 grid(p.n_seq, p.Hq, 16);
+  const dim3 grid(list.most, p.Hq);
   if (p.d == 128)
-    causal_dvec_kernel<128><<<grid, kWarps * 32, 0, s>>>(view(o, p.o), view(d_o, p.o), seqs, dvec,
+    causal_dvec_kernel<128><<<grid, kWarps * 32, 0, s>>>(view(o, p.o), view(d_o, p.o), list.count, list.items, dvec,
                                                          p.total_q);
   else
-    causal_dvec_kernel<64><<<grid, kWarps * 32, 0, s>>>(view(o, p.o), view(d_o, p.o), seqs, dvec,
+    causal_dvec_kernel<64><<<grid, kWarps * 32, 0, s>>>(view(o, p.o), view(d_o, p.o), list.count, list.items, dvec,
                                                         p.total_q);
   return cudaGetLastError();
 }
 
 cudaError_t launch_causal_dq(const CausalProblem& p, const void* q, const void* k, const void* v,
-                             const Seq* seqs, const void* d_o, const float* lse, const float* dvec,
+                             const ItemList& list, const void* d_o, const float* lse, const float* dvec,
                              void* dq, int* err, cudaStream_t s) {
   (void)err;
-  const dim3 grid(p.n_seq, p.Hq, 64);
+  const dim3 grid(list.most, p.Hq);
   if (p.d == 128)
     causal_dq_kernel<128><<<grid, kWarps * 32, 0, s>>>(view(q, p.q), view(k, p.k), view(v, p.v),
-                                                       view(d_o, p.o), seqs, lse, dvec,
+                                                       view(d_o, p.o), list.count, list.items, lse, dvec,
                                                        out(dq, p.q), p.total_q, p.G, p.scale);
   else
     causal_dq_kernel<64><<<grid, kWarps * 32, 0, s>>>(view(q, p.q), view(k, p.k), view(v, p.v),
-                                                      view(d_o, p.o), seqs, lse, dvec,
+                                                      view(d_o, p.o), list.count, list.items, lse, dvec,
                                                       out(dq, p.q), p.total_q, p.G, p.scale);
   return cudaGetLastError();
 }
 
 cudaError_t launch_causal_dkv(const CausalProblem& p, const void* q, const void* k, const void* v,
-                              const Seq* seqs, const void* d_o, const float* lse,
+                              const ItemList& list, const void* d_o, const float* lse,
                               const float* dvec, void* dk, void* dv, int* err, cudaStream_t s) {
   (void)err;
-  const dim3 grid(p.n_seq, p.Hkv, 64);
+  const dim3 grid(list.most, p.Hkv);
   if (p.d == 128)
     causal_dkv_kernel<128><<<grid, kWarps * 32, 0, s>>>(
-        view(q, p.q), view(k, p.k), view(v, p.v), view(d_o, p.o), seqs, lse, dvec, out(dk, p.k),
+        view(q, p.q), view(k, p.k), view(v, p.v), view(d_o, p.o), list.count, list.items, lse, dvec, out(dk, p.k),
         out(dv, p.v), p.total_q, p.G, p.scale);
   else
     causal_dkv_kernel<64><<<grid, kWarps * 32, 0, s>>>(
-        view(q, p.q), view(k, p.k), view(v, p.v), view(d_o, p.o), seqs, lse, dvec, out(dk, p.k),
+        view(q, p.q), view(k, p.k), view(v, p.v), view(d_o, p.o), list.count, list.items, lse, dvec, out(dk, p.k),
         out(dv, p.v), p.total_q, p.G, p.scale);
   return cudaGetLastError();
 }

@@ -3,79 +3,386 @@
 //   s_ab = scale q_a . k_b  (b <= a + Lk - Lq),  lse_a = log sum_b exp s_ab,
 //   o_a = sum_b exp(s_ab - lse_a) v_b
 //
-// One warp per (query row, head); the features lie across the lanes and the
-// running maximum and sum of the softmax in registers (fp32).
+// One pass over the keys in tiles of 128 with a running maximum m and sum l per
+// query (fp32): P = exp2(scale log2(e) s - m) is rounded to bf16 for the product
+// with V, l is summed before that rounding.
+//
+// Design (sm_100a).  A CTA owns two tiles of 128 queries that read the same
+// keys: one tile of tokens for two heads of a group (G even), else 256 tokens of
+// one head.  While the tensor cores work for one tile, the other one's softmax
+// runs.  Warp roles (384 threads):
+//   warps 0-3 / 4-7  softmax of tile A / B: one query row per thread, S from
+//                    TMEM, P back over it (bf16), the lazy rescaling of O, and
+//                    the epilogue [208 registers]
+//   warp 8           TMA producer: Q once, K and V tiles into two rings
+//   warp 9           tcgen05 issuer (one thread): for each tile in turn
+//                    O += P_j V_j, then S_{j+1} = Q K_{j+1}^T over P_j's place
+//   (warps 10, 11 idle: registers are moved by whole warpgroups)
+// TMEM: S of A and B at columns 0 and 128, O at 256 and 384.
+// One thread's products run in order, so S_{j+1} overwrites P_j only after
+// P_j V_j has read it, and S_{j+1}'s completion says that O is at rest: the
+// softmax warps may rescale it then without a wait of their own.
+// The keys behind a sequence's last one belong to others and may hold anything:
+// their scores are replaced by -inf, and their rows of V are cleared in shared
+// memory (0 times NaN would be NaN).
 #include "sla_causal.h"
 #include "sla_ptx.cuh"
 
 namespace sla {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays below 2^8
+constexpr int kThreads = 384;
 
-__device__ __forceinline__ float warp_sum(float x) {
+template <int D>
+struct CfSmem {
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kKSt = D == 128 ? 2 : 5;
+  static constexpr int kVSt = D == 128 ? 3 : 6;
+  static constexpr int kTiles = (2 + kKSt + kVSt) * kTile;  // Q of A and B, K ring, V ring
+};
+template <int D>
+struct CfBars {
+  uint64_t q_full, k_full[CfSmem<D>::kKSt], k_empty[CfSmem<D>::kKSt], v_full[CfSmem<D>::kVSt],
+      v_empty[CfSmem<D>::kVSt], v_fix, s_full[2], p_full[2], o_full[2], mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+template <int D>
+constexpr int kCfTotal = CfSmem<D>::kTiles + int(sizeof(CfBars<D>));
+
+struct CfArgs {
+  const int* count;
+  const Item* items;
+  __nv_bfloat16* o;
+  long long o_row, o_head;
+  float* lse;
+  int total_q, heads, G, pair_heads;  // heads: CTAs per item
+  float scale_log2;
+  int* err;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+    const __grid_constant__ CUtensorMap tm_v, const CfArgs g) {
+  using L = CfSmem<D>;
+  constexpr int kKSt = L::kKSt, kVSt = L::kVSt;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int item = blockIdx.x / g.heads, hx = blockIdx.x % g.heads;
+  if (item >= *g.count) return;
+  const Item it = g.items[item];
+  // the swizzled tiles need 1024-byte alignment: without static shared memory the dynamic
+  // region starts at the CTA's window
+  if ((smem_u32(smem_raw) & 1023u) != 0u) {
+    if (threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
+    return;
+  }
+  uint8_t* sQ = smem_raw;
+  uint8_t* sK = sQ + 2 * L::kTile;
+  uint8_t* sV = sK + kKSt * L::kTile;
+  CfBars<D>& bb = *reinterpret_cast<CfBars<D>*>(smem_raw + L::kTiles);
+  int* err = g.err;
+  volatile int* abort_flag = &bb.abort_flag;
+  const int warp = threadIdx.x / 32, lane = lane_id();
+
+  // the two tiles: first query within the sequence, head, key tiles
+  const int off = it.s.nk - it.s.nq;
+  int a0[2], head[2], n[2];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+  for (int h = 0; h < 2; ++h) {
+    a0[h] = g.pair_heads ? it.tile * 128 : it.tile * 256 + h * 128;
+    head[h] = g.pair_heads ? hx * 2 + h : hx;
+    const int last = min(it.s.nq, a0[h] + 128) + off;  // keys seen by the tile's last query
+    n[h] = a0[h] < it.s.nq && last > 0 ? (last + 127) / 128 : 0;
+  }
+  const int hk = head[0] / g.G;
+  const int nt = max(n[0], n[1]);
+
+  if (warp == 0) tmem_alloc(&bb.tmem_base, 512);
+  if (threadIdx.x == 32) {
+    mbar_init(&bb.q_full, 1);
+    for (int s = 0; s < kKSt; ++s) {
+      mbar_init(&bb.k_full[s], 1);
+      mbar_init(&bb.k_empty[s], 1);
+    }
+    for (int s = 0; s < kVSt; ++s) {
+      mbar_init(&bb.v_full[s], 1);
+      mbar_init(&bb.v_empty[s], 1);
+    }
+    mbar_init(&bb.v_fix, 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&bb.s_full[h], 1);
+      mbar_init(&bb.p_full[h], 128);
+      mbar_init(&bb.o_full[h], 1);
+    }
+    mbar_init(&bb.mma_done, 1);
+    bb.abort_flag = 0;
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bb.tmem_base;
+
+  // registers: 384 threads start with 168 each (64512); 2 x 208 + 80 = 496 per
+  // slot of a warpgroup, 63488 in all
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
+    if (warp == 8 && nt > 0) {
+      // ---------------------------------------------------------------- producer
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        mbar_arrive_expect_tx(&bb.q_full, 2 * L::kTile);
+        for (int h = 0; h < 2; ++h)
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sQ + h * L::kTile + c * 16384, &bb.q_full, &tm_q, c * 64, it.s.q0 + a0[h],
+                        head[h]);
+      }
+      int nk = 0, nv = 0;  // copies issued
+      bool fix = false;
+      auto load_k = [&](int j) -> bool {
+        const int s = j % kKSt;
+        if (j >= kKSt && !mbar_wait(&bb.k_empty[s], ((j / kKSt) + 1) & 1, err, abort_flag))
+          return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bb.k_full[s], L::kTile);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sK + s * L::kTile + c * 16384, &bb.k_full[s], &tm_k, c * 64,
+                        it.s.k0 + j * 128, hk);
+        }
+        ++nk;
+        return true;
+      };
+      auto load_v = [&](int j) -> bool {
+        const int s = j % kVSt;
+        if (j >= kVSt && !mbar_wait(&bb.v_empty[s], ((j / kVSt) + 1) & 1, err, abort_flag))
+          return false;
+        const int valid = it.s.nk - j * 128;
+        uint64_t* bar = valid < 128 ? &bb.v_fix : &bb.v_full[s];
+        uint8_t* dst = sV + s * L::kTile;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, L::kTile);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(dst + c * 16384, bar, &tm_v, c * 64, it.s.k0 + j * 128, hk);
+        }
+        ++nv;
+        if (valid < 128) {  // the sequence's last tile: clear the rows that are not its own
+          fix = true;
+          if (!mbar_wait(&bb.v_fix, 0, err, abort_flag)) return false;
+          for (int c = 0; c < D / 64; ++c)
+            for (int b = valid * 128 + lane * 16; b < 16384; b += 512)
+              *reinterpret_cast<uint4*>(dst + c * 16384 + b) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bb.v_full[s]);
+        }
+        return true;
+      };
+      bool go = load_k(0);
+      for (int j = 0; go && j < nt; ++j) {
+        if (j + 1 < nt) go = load_k(j + 1);
+        if (go) go = load_v(j);
+      }
+      if (bb.abort_flag) {
+        // let copies already in flight land before the CTA exits
+        mbar_wait(&bb.q_full, 0, nullptr, nullptr);
+        for (int j = max(0, nk - kKSt); j < nk; ++j)
+          mbar_wait(&bb.k_full[j % kKSt], (j / kKSt) & 1, nullptr, nullptr);
+        for (int j = max(0, nv - kVSt); j < nv; ++j)
+          if (!(fix && j == nv - 1))
+            mbar_wait(&bb.v_full[j % kVSt], (j / kVSt) & 1, nullptr, nullptr);
+        if (fix) mbar_wait(&bb.v_fix, 0, nullptr, nullptr);
+      }
+    } else if (warp == 9 && lane == 0 && nt > 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
+      bool ok = mbar_wait(&bb.q_full, 0, err, abort_flag);
+      auto issue_s = [&](int h, int j) -> bool {
+        const int s = j % kKSt;
+        if (!mbar_wait(&bb.k_full[s], (j / kKSt) & 1, err, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t qd = desc_kmajor_base(smem_u32(sQ + h * L::kTile));
+        const uint64_t kd = desc_kmajor_base(smem_u32(sK + s * L::kTile));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ss(tmem + h * 128, desc_advance(qd, kmajor_step_bytes(128, ks)),
+                 desc_advance(kd, kmajor_step_bytes(128, ks)), id_s, ks > 0);
+        mma_commit(&bb.s_full[h]);
+        return true;
+      };
+      auto issue_pv = [&](int h, int j) -> bool {
+        const int s = j % kVSt;
+        if (!mbar_wait(&bb.p_full[h], j & 1, err, abort_flag) ||
+            !mbar_wait(&bb.v_full[s], (j / kVSt) & 1, err, abort_flag))
+          return false;
+        tc_fence_after();
+        const uint64_t vd = desc_mnmajor_base(smem_u32(sV + s * L::kTile), 128);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
+                 desc_advance(vd, mnmajor_step_bytes(ks)), id_o, (j | ks) != 0);
+        if (j == n[h] - 1) mma_commit(&bb.o_full[h]);
+        return true;
+      };
+      for (int h = 0; ok && h < 2; ++h)
+        if (n[h] > 0) ok = issue_s(h, 0);
+      if (ok) mma_commit(&bb.k_empty[0]);
+      for (int j = 0; ok && j < nt; ++j) {
+        for (int h = 0; ok && h < 2; ++h) {
+          if (j < n[h]) ok = issue_pv(h, j);
+          if (ok && j + 1 < n[h]) ok = issue_s(h, j + 1);
+        }
+        if (ok) {
+          mma_commit(&bb.v_empty[j % kVSt]);
+          if (j + 1 < nt) mma_commit(&bb.k_empty[(j + 1) % kKSt]);
+        }
+      }
+      mma_commit(&bb.mma_done);
+      mbar_wait(&bb.mma_done, 0, nullptr, nullptr);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    // ---------------------------------------------------------------- softmax
+    const int h = warp >> 2;
+    const int r = threadIdx.x & 127;  // tile row == TMEM lane
+    const int a = (h ? a0[1] : a0[0]) + r, nh = h ? n[1] : n[0];
+    const int lim = a < it.s.nq ? min(it.s.nk, a + off + 1) : 0;  // keys this query sees
+    // keys that every query of the tile sees: tiles below need no mask
+    const int lim0 = min(it.s.nk, (h ? a0[1] : a0[0]) + off + 1);
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_base + h * 128, to = tmem + lane_base + 256 + h * 128;
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+    for (int j = 0; j < nh; ++j) {
+      ok = mbar_wait(&bb.s_full[h], j & 1, err, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      float sv[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        tmem_ld32(ts + c * 32, reinterpret_cast<float(&)[32]>(sv[c * 32]));
+      tmem_ld_wait();
+      if ((j + 1) * 128 > lim0) {
+        const int left = lim - j * 128;
+#pragma unroll
+        for (int e = 0; e < 128; ++e) sv[e] = e < left ? sv[e] : -INFINITY;
+      }
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 128; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], sv[e]);
+      // the scale is positive: the maximum of the raw scores, then scaled
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * g.scale_log2;
+      float alpha = 1.f;
+      if (mx > m_run + kRescaleThreshold) {
+        alpha = exp2f(m_run - mx);  // 0 at first
+        l_run *= alpha;
+        m_run = mx;
+      }
+      const float base = m_run == -INFINITY ? 0.f : m_run;  // a row that sees nothing yet
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = exp2f(fmaf(sv[c * 16 + 2 * e], g.scale_log2, -base));
+          const float y = exp2f(fmaf(sv[c * 16 + 2 * e + 1], g.scale_log2, -base));
+          sum[e & 3] += x + y;
+          pk[e] = pack_bf16(x, y);
+        }
+        tmem_st8(ts + c * 8, pk);
+      }
+      l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          float ov[16];
+          tmem_ld16(to + c0, ov);
+          tmem_ld_wait();
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(ov[e] * alpha);
+          tmem_st16(to + c0, w);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bb.p_full[h]);
+    }
+    // ---------------------------------------------------------------- epilogue
+    if (ok && nh > 0) {
+      ok = mbar_wait(&bb.o_full[h], 0, err, abort_flag);
+      tc_fence_after();
+    }
+    const size_t row = size_t(it.s.q0) + a;
+    const int hd = h ? head[1] : head[0];
+    const bool some = ok && l_run > 0.f;
+    const float inv = some ? 1.f / l_run : 0.f;
+    __nv_bfloat16* po = g.o + row * g.o_row + hd * g.o_head;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+      float ov[32];
+      if (nh > 0) {
+        tmem_ld32(to + c0, ov);
+        tmem_ld_wait();
+      }
+      if (a < it.s.nq) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = some ? pack_bf16(ov[u * 8 + 2 * e] * inv, ov[u * 8 + 2 * e + 1] * inv) : 0u;
+          *reinterpret_cast<uint4*>(po + c0 + u * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    if (a < it.s.nq)
+      g.lse[size_t(hd) * g.total_q + row] =
+          some ? (m_run + __log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_free(tmem, 512);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) causal_fwd_kernel(
-    RowView q, RowView k, RowView v, const Seq* __restrict__ seqs, RowOut o,
-    float* __restrict__ lse, int total_q, int G, float scale) {
-  constexpr int E = D / 32;
-  const Seq sq = seqs[blockIdx.x];
-  const int h = blockIdx.y, lane = lane_id();
-  for (int a = blockIdx.z * kWarps + threadIdx.x / 32; a < sq.nq; a += gridDim.z * kWarps) {
-    float x[E], acc[E], m = -INFINITY, l = 0.f;
-    const size_t row = size_t(sq.q0) + a;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      x[e] = __bfloat162float(q.p[row * q.row + h * q.head + lane * E + e]);
-      acc[e] = 0.f;
-    }
-    const int n = min(sq.nk, a + 1 + sq.nk - sq.nq);
-    for (int b = 0; b < n; ++b) {
-      const size_t kr = size_t(sq.k0) + b;
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        s += x[e] * __bfloat162float(k.p[kr * k.row + h / G * k.head + lane * E + e]);
-      s = warp_sum(s) * scale;
-      const float mn = fmaxf(m, s), c = __expf(m - mn), w = __expf(s - mn);
-      l = l * c + w;
-      m = mn;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        acc[e] = acc[e] * c + w * __bfloat162float(v.p[kr * v.row + h / G * v.head + lane * E + e]);
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o.p[row * o.row + h * o.head + lane * E + e] = __float2bfloat16(acc[e] * inv);
-    if (lane == 0) lse[size_t(h) * total_q + row] = l > 0.f ? m + logf(l) : -INFINITY;
-  }
+cudaError_t launch(const CausalProblem& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                   const CUtensorMap& tv, const CfArgs& a, int most, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      causal_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCfTotal<D>);
+  if (e != cudaSuccess) return e;
+  causal_fwd_kernel<D><<<unsigned(most) * a.heads, kThreads, kCfTotal<D>, s>>>(tq, tk, tv, a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_causal_fwd(const CausalProblem& p, const void* q, const void* k, const void* v,
-                              const Seq* seqs, void* o, float* lse, int* err, cudaStream_t s) {
-  (void)err;
-  using B = __nv_bfloat16;
-  const RowView vq{static_cast<const B*>(q), p.q.row, p.q.head},
-      vk{static_cast<const B*>(k), p.k.row, p.k.head},
-      vv{static_cast<const B*>(v), p.v.row, p.v.head};
-  const RowOut vo{static_cast<B*>(o), p.o.row, p.o.head};
-  const int z = p.max_q < 64 * kWarps ? (p.max_q + kWarps - 1) / kWarps : 64;
-  const dim3 grid(p.n_seq, p.Hq, z);
-  if (p.d == 128)
-    causal_fwd_kernel<128><<<grid, kWarps * 32, 0, s>>>(vq, vk, vv, seqs, vo, lse, p.total_q, p.G,
-                                                        p.scale);
-  else
-    causal_fwd_kernel<64><<<grid, kWarps * 32, 0, s>>>(vq, vk, vv, seqs, vo, lse, p.total_q, p.G,
-                                                       p.scale);
-  return cudaGetLastError();
+                              const ItemList& list, void* o, float* lse, int* err,
+                              cudaStream_t s) {
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap_rows(&tq, q, p.total_q, p.Hq, p.d, p.q, 128) ||
+      !make_tmap_rows(&tk, k, p.total_k, p.Hkv, p.d, p.k, 128) ||
+      !make_tmap_rows(&tv, v, p.total_k, p.Hkv, p.d, p.v, 128))
+    return cudaErrorInvalidValue;
+  const CfArgs a{list.count,
+                 list.items,
+                 static_cast<__nv_bfloat16*>(o),
+                 p.o.row,
+                 p.o.head,
+                 lse,
+                 p.total_q,
+                 pair_heads(p) ? p.Hq / 2 : p.Hq,
+                 p.G,
+                 pair_heads(p),
+                 p.scale_log2,
+                 err};
+  return p.d == 128 ? launch<128>(p, tq, tk, tv, a, list.most, s)
+                    : launch<64>(p, tq, tk, tv, a, list.most, s);
 }
 
 }  // namespace sla

@@ -6,20 +6,90 @@
 namespace sla {
 namespace {
 
+constexpr int kPlanThreads = 1024, kBuckets = 2048;
+
+struct PlanIn {
+  const int32_t *q_off, *k_off, *k_len;
+  int n_seq, total_q, total_k, max_q, shift;
+};
+
 // A sequence whose offsets decrease, leave the tensor or exceed max_q is
 // replaced by an empty one and reported.
-__global__ void causal_plan_kernel(const int32_t* __restrict__ q_off,
-                                   const int32_t* __restrict__ k_off,
-                                   const int32_t* __restrict__ k_len, int n_seq, int total_q,
-                                   int total_k, int max_q, Seq* __restrict__ seqs, int* err) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n_seq) return;
-  const long long q0 = q_off[i], q1 = q_off[i + 1], k0 = k_off[i];
-  const long long k1 = k_len ? k0 + k_len[i] : k_off[i + 1];
-  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= total_q && q1 - q0 <= max_q && k0 >= 0 &&
-                  k1 >= k0 && k1 <= total_k;
-  if (!ok) set_error(err, SLA_ERR_DEVICE);
-  seqs[i] = ok ? Seq{int(q0), int(q1 - q0), int(k0), int(k1 - k0)} : Seq{0, 0, 0, 0};
+__device__ __forceinline__ Seq checked_seq(const PlanIn& in, int i, int* err) {
+  const long long q0 = in.q_off[i], q1 = in.q_off[i + 1], k0 = in.k_off[i];
+  const long long k1 = in.k_len ? k0 + in.k_len[i] : in.k_off[i + 1];
+  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= in.total_q && q1 - q0 <= in.max_q && k0 >= 0 &&
+                  k1 >= k0 && k1 <= in.total_k;
+  if (!ok && lane_id() == 0) set_error(err, SLA_ERR_DEVICE);
+  return ok ? Seq{int(q0), int(q1 - q0), int(k0), int(k1 - k0)} : Seq{0, 0, 0, 0};
+}
+
+// Keys that query tile t sees, or queries that see key tile t, in 128s.
+__device__ __forceinline__ int item_cost(const Seq& s, int t, int tile, bool keys) {
+  const long long off = (long long)s.nk - s.nq;
+  if (keys) {
+    const long long first = max(0ll, (long long)t * tile - off);
+    return first < s.nq ? int((s.nq - first + 127) / 128) : 0;
+  }
+  const long long last = min((long long)s.nq, (long long)(t + 1) * tile) + off;
+  return last > 0 ? int((last + 127) / 128) : 0;
+}
+
+// One CTA per list: the tiles of all sequences by a counting sort on their
+// cost, the most expensive first, so that the long tiles of a causal mask do
+// not start last.  The order among equals is left open: no result depends on
+// it.  A warp takes a sequence, a lane a tile; one sequence of 16384 rows and
+// sixteen short ones take about 4 us either way, bound by the latency of the
+// chain offsets -> histogram -> scan -> scatter.
+__global__ void __launch_bounds__(kPlanThreads) causal_plan_kernel(PlanIn in, CausalPlan plan,
+                                                                   int* err) {
+  __shared__ int hist[kBuckets], warp_sum[32];
+  const bool keys = blockIdx.x == 1;
+  const int tile = keys ? kRowTile : plan.q_tile;
+  Item* items = keys ? plan.k_items : plan.q_items;
+  const int t = threadIdx.x, warp = t / 32, lane = t % 32;
+  for (int b = t; b < kBuckets; b += kPlanThreads) hist[b] = 0;
+  __syncthreads();
+  auto bucket = [&](int cost) { return kBuckets - 1 - min(cost >> in.shift, kBuckets - 1); };
+  for (int i = warp; i < in.n_seq; i += kPlanThreads / 32) {
+    const Seq s = checked_seq(in, i, err);
+    const int n = ((keys ? s.nk : s.nq) + tile - 1) / tile;
+    for (int j = lane; j < n; j += 32) atomicAdd(&hist[bucket(item_cost(s, j, tile, keys))], 1);
+  }
+  __syncthreads();
+  // exclusive sums: two buckets per thread
+  const int a = hist[2 * t], b = hist[2 * t + 1];
+  int sum = a + b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += x;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    int w = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += x;
+    }
+    warp_sum[lane] = w;
+    if (lane == 31) *(keys ? plan.k_count : plan.q_count) = w;
+  }
+  __syncthreads();
+  const int before = sum - a - b + (warp > 0 ? warp_sum[warp - 1] : 0);
+  hist[2 * t] = before;
+  hist[2 * t + 1] = before + a;
+  __syncthreads();
+  for (int i = warp; i < in.n_seq; i += kPlanThreads / 32) {
+    const Seq s = checked_seq(in, i, err);
+    const int n = ((keys ? s.nk : s.nq) + tile - 1) / tile;
+    for (int j = lane; j < n; j += 32) {
+      const int at = atomicAdd(&hist[bucket(item_cost(s, j, tile, keys))], 1);
+      items[at] = Item{s, j, i, 0, 0};
+    }
+  }
 }
 
 __global__ void decay_plan_kernel(const int32_t* __restrict__ off,
@@ -38,9 +108,13 @@ __global__ void decay_plan_kernel(const int32_t* __restrict__ off,
 }  // namespace
 
 cudaError_t launch_causal_plan(const CausalProblem& p, const int32_t* q_off, const int32_t* k_off,
-                               const int32_t* k_len, Seq* seqs, int* err, cudaStream_t s) {
-  causal_plan_kernel<<<(p.n_seq + 255) / 256, 256, 0, s>>>(q_off, k_off, k_len, p.n_seq, p.total_q,
-                                                          p.total_k, p.max_q, seqs, err);
+                               const int32_t* k_len, const CausalPlan& plan, int* err,
+                               cudaStream_t s) {
+  const int most = (p.total_k > p.total_q ? p.total_k : p.total_q) / 128 + 2;
+  int shift = 0;
+  while ((most >> shift) >= kBuckets) ++shift;
+  const PlanIn in{q_off, k_off, k_len, p.n_seq, p.total_q, p.total_k, p.max_q, shift};
+  causal_plan_kernel<<<plan.k_items ? 2 : 1, kPlanThreads, 0, s>>>(in, plan, err);
   return cudaGetLastError();
 }
 

@@ -87,8 +87,8 @@ cudaError_t launch_causal_plan(const CausalProblem& p, const int32_t* q_off, con
                                cudaStream_t s);
 cudaError_t launch_causal_fwd(const CausalProblem& p, const void* q, const void* k, const void* v,
                               const ItemList& list, void* o, float* lse, int* err, cudaStream_t s);
-cudaError_t launch_causal_dvec(const CausalProblem& p, const ItemList& list, const void* o,
-                               const void* d_o, float* dvec, cudaStream_t s);
+cudaError_t launch_causal_dvec(const CausalProblem& p, const void* o, const void* d_o, float* dvec,
+                               cudaStream_t s);
 cudaError_t launch_causal_dq(const CausalProblem& p, const void* q, const void* k, const void* v,
                              const ItemList& list, const void* d_o, const float* lse,
                              const float* dvec, void* dq, int* err, cudaStream_t s);

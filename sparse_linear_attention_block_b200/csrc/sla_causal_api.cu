@@ -192,11 +192,11 @@ sla_status sla_causal_backward(const sla_causal_shape* shape, const void* q, con
   int* counts = at<int>(workspace, L.counts);
   Item *items = at<Item>(workspace, L.items), *kitems = at<Item>(workspace, L.kitems);
   float* dvec = at<float>(workspace, L.dvec);
-  const CausalPlan plan{kRowTile, items, counts, kitems, counts + 1};
+  const CausalPlan plan{fwd_tile(p), items, counts, kitems, counts + 1};
   SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, nullptr, plan, err, s));
-  const ItemList list{counts, items, int(most_items(p.total_q, kRowTile, p.n_seq))};
+  const ItemList list{counts, items, int(most_items(p.total_q, plan.q_tile, p.n_seq))};
   const ItemList klist{counts + 1, kitems, int(most_items(p.total_k, kRowTile, p.n_seq))};
-  SLA_LAUNCH("causal_dvec", s, launch_causal_dvec(p, list, o, d_o, dvec, s));
+  SLA_LAUNCH("causal_dvec", s, launch_causal_dvec(p, o, d_o, dvec, s));
   SLA_LAUNCH("causal_dkv", s,
              launch_causal_dkv(p, q, k, v, klist, d_o, lse, dvec, dk, dv, err, s));
   SLA_LAUNCH("causal_dq", s, launch_causal_dq(p, q, k, v, list, d_o, lse, dvec, dq, err, s));

@@ -5,120 +5,650 @@
 //   dk_b = scale sum_{h of the group, a} dS_ab q_a,  dv_b = sum_{h, a} P_ab do_a
 //
 // Two kernels, one over queries and one over keys, so that every sum has one
-// owner: no atomics, equal inputs give equal bits.
+// owner: no atomics, equal inputs give equal bits, and the gradients leave as
+// bf16 once.  That costs seven tile products where one kernel with atomic dQ
+// needs five.  P and dS are rounded to bf16 for their products; the scores, the
+// statistics and all sums are fp32.
 #include "sla_causal.h"
 #include "sla_ptx.cuh"
 
 namespace sla {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 384;
+constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
+struct CbArgs {
+  const int* count;
+  const Item* items;
+  const float *lse, *dvec;
+  RowOut out0, out1;  // dq; or dk and dv
+  int total_q, heads, G, pair_heads;
+  float scale, scale_log2;
+  int* err;
+};
 
-template <int E>
-__device__ __forceinline__ void load_row(float (&x)[E], const RowView& t, size_t row, int head) {
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    x[e] = __bfloat162float(t.p[row * t.row + head * t.head + lane_id() * E + e]);
-}
-template <int E>
-__device__ __forceinline__ void store_row(const float (&x)[E], const RowOut& t, size_t row,
-                                          int head, float f) {
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    t.p[row * t.row + head * t.head + lane_id() * E + e] = __float2bfloat16(x[e] * f);
-}
-template <int E>
-__device__ __forceinline__ float dot(const float (&x)[E], const float (&y)[E]) {
+// ------------------------------------------------------------------ D
+// One group of D / 8 lanes per (row, head), 16 bytes per lane and tensor: bound
+// by the bytes of o and do.
+template <int D>
+__global__ void __launch_bounds__(256) causal_dvec_kernel(RowView o, RowView d_o, float* dvec,
+                                                          int total_q, int Hq) {
+  constexpr int kL = D / 8;
+  const long long i = (long long)blockIdx.x * (256 / kL) + threadIdx.x / kL;
+  const int x = threadIdx.x % kL;
+  const bool in = i < (long long)total_q * Hq;
+  const int h = in ? int(i % Hq) : 0;
+  const long long row = in ? i / Hq : 0;
+  const uint4 a = *reinterpret_cast<const uint4*>(o.p + row * o.row + h * o.head + x * 8);
+  const uint4 b = *reinterpret_cast<const uint4*>(d_o.p + row * d_o.row + h * d_o.head + x * 8);
+  const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
   float s = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) s += x[e] * y[e];
-  return warp_sum(s);
+  for (int e = 0; e < 4; ++e)
+    s += bf16_lo(aw[e]) * bf16_lo(bw[e]) + bf16_hi(aw[e]) * bf16_hi(bw[e]);
+#pragma unroll
+  for (int k = kL / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+  if (in && x == 0) dvec[size_t(h) * total_q + row] = s;
 }
 
+// Clear rows [valid, rows) of a swizzled tile of D / 64 chunks (whole warp).
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) causal_dvec_kernel(RowView o, RowView d_o,
-                                                                  const int* __restrict__ count, const Item* __restrict__ items,
-                                                                  float* __restrict__ dvec,
-                                                                  int total_q) {
-  if (int(blockIdx.x) >= *count) return;
-  const Seq sq = items[blockIdx.x].s;
-  const int t0 = items[blockIdx.x].tile * kRowTile;
-  const int h = blockIdx.y;
-  for (int a = t0 + threadIdx.x / 32; a < min(sq.nq, t0 + kRowTile); a += kWarps) {
-    float x[D / 32], y[D / 32];
-    load_row(x, o, size_t(sq.q0) + a, h);
-    load_row(y, d_o, size_t(sq.q0) + a, h);
-    const float s = dot(x, y);
-    if (lane_id() == 0) dvec[size_t(h) * total_q + sq.q0 + a] = s;
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int rows, int valid) {
+  for (int c = 0; c < D / 64; ++c)
+    for (int b = valid * 128 + int(lane_id()) * 16; b < rows * 128; b += 512)
+      *reinterpret_cast<uint4*>(tile + c * rows * 128 + b) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// 32 TMEM columns of a thread's row, times f, as bf16 to global memory.
+__device__ __forceinline__ void store_row32(uint32_t taddr, bool have, bool write, float f,
+                                            __nv_bfloat16* dst) {
+  float v[32];
+  if (have) {
+    tmem_ld32(taddr, v);
+    tmem_ld_wait();
+  }
+  if (!write) return;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = have ? pack_bf16(v[u * 8 + 2 * e] * f, v[u * 8 + 2 * e + 1] * f) : 0u;
+    *reinterpret_cast<uint4*>(dst + u * 8) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
+// ------------------------------------------------------------------ dQ
+// A CTA owns two tiles of 128 queries that read the same keys (as in the
+// forward) and walks the keys in tiles of 64.  Per tile and step:
+//   S = Q K^T, dP = dO V^T (M = 128, N = 64), dS = P (dP - D) over S's place,
+//   dQ += dS K (dS from TMEM, M = 128, N = d)
+// The two tiles alternate: one's products run during the other's arithmetic.
+// TMEM: S 0, dP 64 of tile A, 128 and 192 of B; dQ at 256 and 384.  A product
+// with N = 64 reads 6 KB of shared memory per 32 cycles of the tensor pipe, more
+// than the 128 bytes per cycle that there are, so the tensor pipe is bounded to
+// about 3/4 of its rate; 128 keys do not fit in TMEM for two tiles, and one tile
+// alone would double the K/V traffic from L2.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) causal_dq_kernel(
-    RowView q, RowView k, RowView v, RowView d_o, const int* __restrict__ count, const Item* __restrict__ items,
-    const float* __restrict__ lse, const float* __restrict__ dvec, RowOut dq, int total_q, int G,
-    float scale) {
-  constexpr int E = D / 32;
-  if (int(blockIdx.x) >= *count) return;
-  const Seq sq = items[blockIdx.x].s;
-  const int t0 = items[blockIdx.x].tile * kRowTile;
-  const int h = blockIdx.y;
-  for (int a = t0 + threadIdx.x / 32; a < min(sq.nq, t0 + kRowTile); a += kWarps) {
-    const size_t row = size_t(sq.q0) + a;
-    float x[E], g[E], acc[E] = {};
-    load_row(x, q, row, h);
-    load_row(g, d_o, row, h);
-    const float l = lse[size_t(h) * total_q + row], dd = dvec[size_t(h) * total_q + row];
-    const int n = min(sq.nk, a + 1 + sq.nk - sq.nq);
-    for (int b = 0; b < n; ++b) {
-      float kk[E], vv[E];
-      load_row(kk, k, size_t(sq.k0) + b, h / G);
-      load_row(vv, v, size_t(sq.k0) + b, h / G);
-      const float ds = __expf(dot(x, kk) * scale - l) * (dot(g, vv) - dd);
+struct DqSmem {
+  static constexpr int kQ = 128 * D * 2, kKV = 64 * D * 2;
+  static constexpr int kSt = D == 128 ? 3 : 6;
+  static constexpr int kTiles = 4 * kQ + 2 * kSt * kKV;  // Q A, Q B, dO A, dO B, K ring, V ring
+};
+template <int D>
+struct DqBars {
+  static constexpr int kSt = DqSmem<D>::kSt;
+  uint64_t q_full, k_full[kSt], k_empty[kSt], v_full[kSt], v_empty[kSt], k_fix, s_full[2],
+      ds_full[2], o_full[2], mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+template <int D>
+constexpr int kDqTotal = DqSmem<D>::kTiles + int(sizeof(DqBars<D>));
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const CbArgs g) {
+  using L = DqSmem<D>;
+  constexpr int kSt = L::kSt;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int item = blockIdx.x / g.heads, hx = blockIdx.x % g.heads;
+  if (item >= *g.count) return;
+  const Item it = g.items[item];
+  if ((smem_u32(smem_raw) & 1023u) != 0u) {
+    if (threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
+    return;
+  }
+  uint8_t* sQ = smem_raw;
+  uint8_t* sDO = sQ + 2 * L::kQ;
+  uint8_t* sK = sDO + 2 * L::kQ;
+  uint8_t* sV = sK + kSt * L::kKV;
+  DqBars<D>& bb = *reinterpret_cast<DqBars<D>*>(smem_raw + L::kTiles);
+  int* err = g.err;
+  volatile int* abort_flag = &bb.abort_flag;
+  const int warp = threadIdx.x / 32, lane = lane_id();
+
+  const int off = it.s.nk - it.s.nq;
+  int a0[2], head[2], n[2];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += ds * kk[e];
+  for (int h = 0; h < 2; ++h) {
+    a0[h] = g.pair_heads ? it.tile * 128 : it.tile * 256 + h * 128;
+    head[h] = g.pair_heads ? hx * 2 + h : hx;
+    const int last = min(it.s.nq, a0[h] + 128) + off;
+    n[h] = a0[h] < it.s.nq && last > 0 ? (last + 63) / 64 : 0;
+  }
+  const int hk = head[0] / g.G;
+  const int nt = max(n[0], n[1]);
+
+  if (warp == 0) tmem_alloc(&bb.tmem_base, 512);
+  if (threadIdx.x == 32) {
+    mbar_init(&bb.q_full, 1);
+    for (int s = 0; s < kSt; ++s) {
+      mbar_init(&bb.k_full[s], 1);
+      mbar_init(&bb.k_empty[s], 1);
+      mbar_init(&bb.v_full[s], 1);
+      mbar_init(&bb.v_empty[s], 1);
     }
-    store_row(acc, dq, row, h, scale);
+    mbar_init(&bb.k_fix, 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&bb.s_full[h], 1);
+      mbar_init(&bb.ds_full[h], 128);
+      mbar_init(&bb.o_full[h], 1);
+    }
+    mbar_init(&bb.mma_done, 1);
+    bb.abort_flag = 0;
+    fence_barrier_init();
   }
-}
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bb.tmem_base;
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) causal_dkv_kernel(
-    RowView q, RowView k, RowView v, RowView d_o, const int* __restrict__ count, const Item* __restrict__ items,
-    const float* __restrict__ lse, const float* __restrict__ dvec, RowOut dk, RowOut dv,
-    int total_q, int G, float scale) {
-  constexpr int E = D / 32;
-  if (int(blockIdx.x) >= *count) return;
-  const Seq sq = items[blockIdx.x].s;
-  const int t0 = items[blockIdx.x].tile * kRowTile;
-  const int hk = blockIdx.y;
-  for (int b = t0 + threadIdx.x / 32; b < min(sq.nk, t0 + kRowTile); b += kWarps) {
-    float kk[E], vv[E], ak[E] = {}, av[E] = {};
-    load_row(kk, k, size_t(sq.k0) + b, hk);
-    load_row(vv, v, size_t(sq.k0) + b, hk);
-    for (int h = hk * G; h < (hk + 1) * G; ++h)
-      for (int a = max(0, b - (sq.nk - sq.nq)); a < sq.nq; ++a) {
-        const size_t row = size_t(sq.q0) + a;
-        float x[E], g[E];
-        load_row(x, q, row, h);
-        load_row(g, d_o, row, h);
-        const float p = __expf(dot(x, kk) * scale - lse[size_t(h) * total_q + row]);
-        const float ds = p * (dot(g, vv) - dvec[size_t(h) * total_q + row]);
+  // registers: 168 at launch; 2 x 208 + 80 per slot of a warpgroup
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
+    if (warp == 8 && nt > 0) {
+      // ---------------------------------------------------------------- producer
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bb.q_full, 4 * L::kQ);
+        for (int h = 0; h < 2; ++h)
+          for (int c = 0; c < D / 64; ++c) {
+            tma_load_3d(sQ + h * L::kQ + c * 16384, &bb.q_full, &tm_q, c * 64, it.s.q0 + a0[h],
+                        head[h]);
+            tma_load_3d(sDO + h * L::kQ + c * 16384, &bb.q_full, &tm_do, c * 64, it.s.q0 + a0[h],
+                        head[h]);
+          }
+      }
+      int nk = 0, nv = 0;
+      bool fix = false, go = true;
+      for (int j = 0; go && j < nt; ++j) {
+        const int s = j % kSt;
+        const uint32_t ph = ((j / kSt) + 1) & 1;
+        if (j >= kSt && !(go = mbar_wait(&bb.k_empty[s], ph, err, abort_flag))) break;
+        const int valid = it.s.nk - j * 64;
+        uint8_t* dst = sK + s * L::kKV;
+        uint64_t* bar = valid < 64 ? &bb.k_fix : &bb.k_full[s];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, L::kKV);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(dst + c * 8192, bar, &tm_k, c * 64, it.s.k0 + j * 64, hk);
+        }
+        ++nk;
+        if (valid < 64) {  // the sequence's last keys: clear the rows behind them (0 times NaN)
+          fix = true;
+          if (!(go = mbar_wait(&bb.k_fix, 0, err, abort_flag))) break;
+          clear_rows<D>(dst, 64, valid);
+          if (lane == 0) mbar_arrive(&bb.k_full[s]);
+        }
+        if (j >= kSt && !(go = mbar_wait(&bb.v_empty[s], ph, err, abort_flag))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bb.v_full[s], L::kKV);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sV + s * L::kKV + c * 8192, &bb.v_full[s], &tm_v, c * 64,
+                        it.s.k0 + j * 64, hk);
+        }
+        ++nv;
+      }
+      if (bb.abort_flag) {
+        // let copies already in flight land before the CTA exits
+        mbar_wait(&bb.q_full, 0, nullptr, nullptr);
+        for (int j = max(0, nk - kSt); j < nk; ++j)
+          if (!(fix && j == nk - 1))
+            mbar_wait(&bb.k_full[j % kSt], (j / kSt) & 1, nullptr, nullptr);
+        if (fix) mbar_wait(&bb.k_fix, 0, nullptr, nullptr);
+        for (int j = max(0, nv - kSt); j < nv; ++j)
+          mbar_wait(&bb.v_full[j % kSt], (j / kSt) & 1, nullptr, nullptr);
+      }
+    } else if (warp == 9 && lane == 0 && nt > 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_q = idesc_bf16(128, D, 0, 1);
+      bool ok = mbar_wait(&bb.q_full, 0, err, abort_flag);
+      auto issue_s = [&](int h, int j) -> bool {  // S and dP
+        const int s = j % kSt;
+        const uint32_t ph = (j / kSt) & 1;
+        if (!mbar_wait(&bb.k_full[s], ph, err, abort_flag) ||
+            !mbar_wait(&bb.v_full[s], ph, err, abort_flag))
+          return false;
+        tc_fence_after();
+        const uint64_t qd = desc_kmajor_base(smem_u32(sQ + h * L::kQ)),
+                       od = desc_kmajor_base(smem_u32(sDO + h * L::kQ)),
+                       kd = desc_kmajor_base(smem_u32(sK + s * L::kKV)),
+                       vd = desc_kmajor_base(smem_u32(sV + s * L::kKV));
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          ak[e] += ds * x[e];
-          av[e] += p * g[e];
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t qa = kmajor_step_bytes(128, ks), ka = kmajor_step_bytes(64, ks);
+          mma_ss(tmem + h * 128, desc_advance(qd, qa), desc_advance(kd, ka), id_s, ks > 0);
+          mma_ss(tmem + h * 128 + 64, desc_advance(od, qa), desc_advance(vd, ka), id_s, ks > 0);
+        }
+        mma_commit(&bb.s_full[h]);
+        return true;
+      };
+      auto issue_dq = [&](int h, int j) -> bool {
+        if (!mbar_wait(&bb.ds_full[h], j & 1, err, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t kd = desc_mnmajor_base(smem_u32(sK + (j % kSt) * L::kKV), 64);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
+                 desc_advance(kd, mnmajor_step_bytes(ks)), id_q, (j | ks) != 0);
+        if (j == n[h] - 1) mma_commit(&bb.o_full[h]);
+        return true;
+      };
+      for (int h = 0; ok && h < 2; ++h)
+        if (n[h] > 0) ok = issue_s(h, 0);
+      if (ok) mma_commit(&bb.v_empty[0]);
+      for (int j = 0; ok && j < nt; ++j) {
+        for (int h = 0; ok && h < 2; ++h) {
+          if (j < n[h]) ok = issue_dq(h, j);
+          if (ok && j + 1 < n[h]) ok = issue_s(h, j + 1);
+        }
+        if (ok) {
+          mma_commit(&bb.k_empty[j % kSt]);
+          if (j + 1 < nt) mma_commit(&bb.v_empty[(j + 1) % kSt]);
         }
       }
-    store_row(ak, dk, size_t(sq.k0) + b, hk, scale);
-    store_row(av, dv, size_t(sq.k0) + b, hk, 1.f);
+      mma_commit(&bb.mma_done);
+      mbar_wait(&bb.mma_done, 0, nullptr, nullptr);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    // ---------------------------------------------------------------- dS
+    const int h = warp >> 2, r = threadIdx.x & 127;
+    const int a = (h ? a0[1] : a0[0]) + r, nh = h ? n[1] : n[0], hd = h ? head[1] : head[0];
+    const bool real = a < it.s.nq;
+    const int lim = real ? min(it.s.nk, a + off + 1) : 0;
+    const int lim0 = min(it.s.nk, (h ? a0[1] : a0[0]) + off + 1);
+    const size_t row = size_t(it.s.q0) + a;
+    const float base = real ? g.lse[size_t(hd) * g.total_q + row] * kLog2e : 0.f;
+    const float dd = real ? g.dvec[size_t(hd) * g.total_q + row] : 0.f;
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_base + h * 128, to = tmem + lane_base + 256 + h * 128;
+    bool ok = true;
+    for (int j = 0; j < nh; ++j) {
+      ok = mbar_wait(&bb.s_full[h], j & 1, err, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      float sv[64], pv[64];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld32(ts + c * 32, reinterpret_cast<float(&)[32]>(sv[c * 32]));
+        tmem_ld32(ts + 64 + c * 32, reinterpret_cast<float(&)[32]>(pv[c * 32]));
+      }
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 64; ++e)
+        sv[e] = exp2f(fmaf(sv[e], g.scale_log2, -base)) * (pv[e] - dd);
+      if ((j + 1) * 64 > lim0) {
+        const int left = lim - j * 64;
+#pragma unroll
+        for (int e = 0; e < 64; ++e) sv[e] = e < left ? sv[e] : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pk[e] = pack_bf16(sv[c * 16 + 2 * e], sv[c * 16 + 2 * e + 1]);
+        tmem_st8(ts + c * 8, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bb.ds_full[h]);
+    }
+    if (ok && nh > 0) {
+      ok = mbar_wait(&bb.o_full[h], 0, err, abort_flag);
+      tc_fence_after();
+    }
+    __nv_bfloat16* dst = g.out0.p + row * g.out0.row + hd * g.out0.head;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) store_row32(to + c0, ok && nh > 0, real, g.scale, dst + c0);
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_free(tmem, 512);
+}
+
+// ------------------------------------------------------------------ dK, dV
+// A CTA owns 128 keys of one key head and walks the query tiles (128) that see
+// them, of every head of the group.  Per step i:
+//   S^T = K Q^T, dP^T = V dO^T      (M = 128 keys, N = 128 queries)
+//   P^T -> TMEM over S^T, dS^T = P^T (dP^T - D) -> TMEM over dP^T
+//   dV += P^T dO, dK += dS^T Q      (A from TMEM, N = d)
+// The tensor pipe runs dV(i), S(i + 1), dK(i), dP(i + 1): the exponentials of
+// step i + 1 go on while dK(i) and dP(i + 1) run, the slopes of i + 1 while
+// dV(i + 1) and S(i + 2) do, so that one set of TMEM buffers keeps it fed.
+// TMEM: S^T 0, dP^T 128, dV 256, dK 384.  Each warpgroup takes 64 query columns
+// of every step and writes P^T and dS^T over the first half of its own columns.
+// Warp 10: the statistics lse and D of a step's queries into shared memory.
+template <int D>
+struct DkSmem {
+  static constexpr int kT = 128 * D * 2;
+  static constexpr int kQSt = 3, kOSt = 2, kLSt = 2;
+  static constexpr int kTiles = (2 + kQSt + kOSt) * kT;  // K, V, Q ring, dO ring
+  static constexpr int kLd = kLSt * 2 * 128 * 4;         // lse log2(e), then D, per stage
+};
+template <int D>
+struct DkBars {
+  using L = DkSmem<D>;
+  uint64_t kv_full, q_full[L::kQSt], q_empty[L::kQSt], o_full[L::kOSt], o_empty[L::kOSt],
+      l_full[L::kLSt], l_empty[L::kLSt], q_fix, o_fix, s_full, p_full, dp_full, ds_full, acc_full, mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+template <int D>
+constexpr int kDkTotal = DkSmem<D>::kTiles + DkSmem<D>::kLd + int(sizeof(DkBars<D>));
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const CbArgs g) {
+  using L = DkSmem<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const int item = blockIdx.x / g.heads, hk = blockIdx.x % g.heads;
+  if (item >= *g.count) return;
+  const Item it = g.items[item];
+  if ((smem_u32(smem_raw) & 1023u) != 0u) {
+    if (threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
+    return;
+  }
+  uint8_t* sK = smem_raw;
+  uint8_t* sV = sK + L::kT;
+  uint8_t* sQ = sV + L::kT;
+  uint8_t* sDO = sQ + L::kQSt * L::kT;
+  float* sLd = reinterpret_cast<float*>(smem_raw + L::kTiles);
+  DkBars<D>& bb = *reinterpret_cast<DkBars<D>*>(smem_raw + L::kTiles + L::kLd);
+  int* err = g.err;
+  volatile int* abort_flag = &bb.abort_flag;
+  const int warp = threadIdx.x / 32, lane = lane_id();
+
+  const int off = it.s.nk - it.s.nq, b0 = it.tile * 128;
+  // query tiles that see the first of these keys, and the last tile
+  const int qt0 = max(0, b0 - off) / 128;
+  const int nq = max(0, b0 - off) < it.s.nq ? (it.s.nq + 127) / 128 - qt0 : 0;
+  const int n = nq * g.G;  // steps: the group's heads one after the other
+
+  if (warp == 0) tmem_alloc(&bb.tmem_base, 512);
+  if (threadIdx.x == 32) {
+    mbar_init(&bb.kv_full, 1);
+    for (int s = 0; s < L::kQSt; ++s) {
+      mbar_init(&bb.q_full[s], 1);
+      mbar_init(&bb.q_empty[s], 1);
+    }
+    for (int s = 0; s < L::kOSt; ++s) {
+      mbar_init(&bb.o_full[s], 1);
+      mbar_init(&bb.o_empty[s], 1);
+    }
+    for (int s = 0; s < L::kLSt; ++s) {
+      mbar_init(&bb.l_full[s], 32);
+      mbar_init(&bb.l_empty[s], 8);
+    }
+    mbar_init(&bb.q_fix, 1);
+    mbar_init(&bb.o_fix, 1);
+    mbar_init(&bb.s_full, 1);
+    mbar_init(&bb.p_full, 256);
+    mbar_init(&bb.dp_full, 1);
+    mbar_init(&bb.ds_full, 256);
+    mbar_init(&bb.acc_full, 1);
+    mbar_init(&bb.mma_done, 1);
+    bb.abort_flag = 0;
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bb.tmem_base;
+
+  // registers: 168 at launch; 2 x 208 + 80 per slot of a warpgroup
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
+    if (warp == 8 && n > 0) {
+      // ---------------------------------------------------------------- producer
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bb.kv_full, 2 * L::kT);
+        for (int c = 0; c < D / 64; ++c) {
+          tma_load_3d(sK + c * 16384, &bb.kv_full, &tm_k, c * 64, it.s.k0 + b0, hk);
+          tma_load_3d(sV + c * 16384, &bb.kv_full, &tm_v, c * 64, it.s.k0 + b0, hk);
+        }
+      }
+      int i = 0, lq = 0, lo = 0;        // copies issued
+      int fixq = -1, fixo = -1, fixes = 0;  // the last ones through the fix barriers
+      bool go = true;
+      // a tile of Q or dO; the last one of a sequence has the rows behind it cleared
+      auto load = [&](uint8_t* dst, uint64_t* full, uint64_t* fix, const CUtensorMap& tm, int tile,
+                      int h) -> bool {
+        const int valid = it.s.nq - tile * 128;
+        uint64_t* bar = valid < 128 ? fix : full;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, L::kT);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(dst + c * 16384, bar, &tm, c * 64, it.s.q0 + tile * 128, h);
+        }
+        return true;
+      };
+      auto finish = [&](uint8_t* dst, uint64_t* full, uint64_t* fix, int tile) -> bool {
+        const int valid = it.s.nq - tile * 128;
+        if (valid >= 128) return true;
+        if (!mbar_wait(fix, fixes & 1, err, abort_flag)) return false;
+        clear_rows<D>(dst, 128, valid);
+        if (lane == 0) mbar_arrive(full);
+        return true;
+      };
+      for (int hg = 0; go && hg < g.G; ++hg)
+        for (int t = 0; go && t < nq; ++t, ++i) {
+          const int tile = qt0 + t, h = hk * g.G + hg, sq = i % L::kQSt, so = i % L::kOSt;
+          uint8_t *dq = sQ + sq * L::kT, *dgo = sDO + so * L::kT;
+          const bool part = it.s.nq - tile * 128 < 128;
+          if (i >= L::kQSt &&
+              !(go = mbar_wait(&bb.q_empty[sq], ((i / L::kQSt) + 1) & 1, err, abort_flag)))
+            break;
+          load(dq, &bb.q_full[sq], &bb.q_fix, tm_q, tile, h);
+          ++lq;
+          if (part) fixq = i;
+          if (i >= L::kOSt &&
+              !(go = mbar_wait(&bb.o_empty[so], ((i / L::kOSt) + 1) & 1, err, abort_flag)))
+            break;
+          load(dgo, &bb.o_full[so], &bb.o_fix, tm_do, tile, h);
+          ++lo;
+          if (part) fixo = i;
+          if (!(go = finish(dq, &bb.q_full[sq], &bb.q_fix, tile))) break;
+          if (!(go = finish(dgo, &bb.o_full[so], &bb.o_fix, tile))) break;
+          if (part) ++fixes;
+        }
+      if (bb.abort_flag) {
+        // let copies already in flight land before the CTA exits
+        mbar_wait(&bb.kv_full, 0, nullptr, nullptr);
+        for (int k = max(0, lq - L::kQSt); k < lq; ++k)
+          if (k != fixq) mbar_wait(&bb.q_full[k % L::kQSt], (k / L::kQSt) & 1, nullptr, nullptr);
+        for (int k = max(0, lo - L::kOSt); k < lo; ++k)
+          if (k != fixo) mbar_wait(&bb.o_full[k % L::kOSt], (k / L::kOSt) & 1, nullptr, nullptr);
+        if (fixq == lq - 1 && lq > 0) mbar_wait(&bb.q_fix, fixes & 1, nullptr, nullptr);
+        if (fixo == lo - 1 && lo > 0) mbar_wait(&bb.o_fix, fixes & 1, nullptr, nullptr);
+      }
+    } else if (warp == 9 && lane == 0 && n > 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_g = idesc_bf16(128, D, 0, 1);
+      const uint64_t kd = desc_kmajor_base(smem_u32(sK)), vd = desc_kmajor_base(smem_u32(sV));
+      auto issue_s = [&](int i) -> bool {
+        const int s = i % L::kQSt;
+        if (!mbar_wait(&bb.q_full[s], (i / L::kQSt) & 1, err, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t qd = desc_kmajor_base(smem_u32(sQ + s * L::kT));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ss(tmem, desc_advance(kd, kmajor_step_bytes(128, ks)),
+                 desc_advance(qd, kmajor_step_bytes(128, ks)), id_s, ks > 0);
+        mma_commit(&bb.s_full);
+        return true;
+      };
+      auto issue_dp = [&](int i) -> bool {
+        const int s = i % L::kOSt;
+        if (!mbar_wait(&bb.o_full[s], (i / L::kOSt) & 1, err, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t od = desc_kmajor_base(smem_u32(sDO + s * L::kT));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ss(tmem + 128, desc_advance(vd, kmajor_step_bytes(128, ks)),
+                 desc_advance(od, kmajor_step_bytes(128, ks)), id_s, ks > 0);
+        mma_commit(&bb.dp_full);
+        return true;
+      };
+      // acc += A(TMEM) * B, A's k-step ks (16 queries) at 8 ks of the warpgroup's half
+      auto issue_g = [&](uint32_t acc, uint32_t a, uint8_t* tile, int i) {
+        tc_fence_after();
+        const uint64_t bd = desc_mnmajor_base(smem_u32(tile), 128);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts(acc, a + (ks & 3) * 8 + (ks >> 2) * 64, desc_advance(bd, mnmajor_step_bytes(ks)),
+                 id_g, (i | ks) != 0);
+      };
+      bool ok = mbar_wait(&bb.kv_full, 0, err, abort_flag) && issue_s(0) && issue_dp(0);
+      for (int i = 0; ok && i < n; ++i) {
+        if (!(ok = mbar_wait(&bb.p_full, i & 1, err, abort_flag))) break;
+        issue_g(tmem + 256, tmem, sDO + (i % L::kOSt) * L::kT, i);
+        mma_commit(&bb.o_empty[i % L::kOSt]);
+        if (i + 1 < n && !(ok = issue_s(i + 1))) break;
+        if (!(ok = mbar_wait(&bb.ds_full, i & 1, err, abort_flag))) break;
+        issue_g(tmem + 384, tmem + 128, sQ + (i % L::kQSt) * L::kT, i);
+        mma_commit(&bb.q_empty[i % L::kQSt]);
+        if (i + 1 < n) ok = issue_dp(i + 1);
+      }
+      if (ok) mma_commit(&bb.acc_full);
+      mma_commit(&bb.mma_done);
+      mbar_wait(&bb.mma_done, 0, nullptr, nullptr);
+    } else if (warp == 10 && n > 0) {
+      // ---------------------------------------------------------------- statistics
+      for (int i = 0; i < n; ++i) {
+        if (i >= L::kLSt &&
+            !mbar_wait(&bb.l_empty[i % L::kLSt], ((i / L::kLSt) + 1) & 1, err, abort_flag))
+          break;
+        const int h = hk * g.G + i / nq, a = (qt0 + i % nq) * 128;
+        float* dst = sLd + (i % L::kLSt) * 256;
+        const size_t at = size_t(h) * g.total_q + it.s.q0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int x = a + e * 32 + lane;
+          dst[e * 32 + lane] = x < it.s.nq ? g.lse[at + x] * kLog2e : 0.f;
+          dst[128 + e * 32 + lane] = x < it.s.nq ? g.dvec[at + x] : 0.f;
+        }
+        mbar_arrive(&bb.l_full[i % L::kLSt]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+    // ---------------------------------------------------------------- P, dS
+    const int w = warp >> 2, r = threadIdx.x & 127;
+    const int b = b0 + r;
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_base + w * 64, tp = ts + 128;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int a = (qt0 + i % nq) * 128 + w * 64;  // first query of these columns
+      const float* ld = sLd + (i % L::kLSt) * 256 + w * 64;
+      ok = mbar_wait(&bb.l_full[i % L::kLSt], (i / L::kLSt) & 1, err, abort_flag) &&
+           mbar_wait(&bb.s_full, i & 1, err, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      float p[64];
+      tmem_ld32(ts, reinterpret_cast<float(&)[32]>(p[0]));
+      tmem_ld32(ts + 32, reinterpret_cast<float(&)[32]>(p[32]));
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(ld + e);
+        p[e] = exp2f(fmaf(p[e], g.scale_log2, -l.x));
+        p[e + 1] = exp2f(fmaf(p[e + 1], g.scale_log2, -l.y));
+        p[e + 2] = exp2f(fmaf(p[e + 2], g.scale_log2, -l.z));
+        p[e + 3] = exp2f(fmaf(p[e + 3], g.scale_log2, -l.w));
+      }
+      // query a + e sees key b where e >= lo, and is one of the sequence's where e < hi
+      const int lo = b - off - a, hi = it.s.nq - a;
+      const bool edge = b0 + 127 - off > a || hi < 64;
+      if (edge) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) p[e] = e >= lo && e < hi ? p[e] : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pk[e] = pack_bf16(p[c * 16 + 2 * e], p[c * 16 + 2 * e + 1]);
+        tmem_st8(ts + c * 8, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bb.p_full);
+      ok = mbar_wait(&bb.dp_full, i & 1, err, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      float dp[64];
+      tmem_ld32(tp, reinterpret_cast<float(&)[32]>(dp[0]));
+      tmem_ld32(tp + 32, reinterpret_cast<float(&)[32]>(dp[32]));
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        const float4 d = *reinterpret_cast<const float4*>(ld + 128 + e);
+        p[e] *= dp[e] - d.x;
+        p[e + 1] *= dp[e + 1] - d.y;
+        p[e + 2] *= dp[e + 2] - d.z;
+        p[e + 3] *= dp[e + 3] - d.w;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bb.l_empty[i % L::kLSt]);
+      if (edge) {  // 0 times what a foreign row of dO gives
+#pragma unroll
+        for (int e = 0; e < 64; ++e) p[e] = e >= lo && e < hi ? p[e] : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pk[e] = pack_bf16(p[c * 16 + 2 * e], p[c * 16 + 2 * e + 1]);
+        tmem_st8(tp + c * 8, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bb.ds_full);
+    }
+    if (ok && n > 0) {
+      ok = mbar_wait(&bb.acc_full, 0, err, abort_flag);
+      tc_fence_after();
+    }
+    // warpgroup 0 writes dV, 1 dK
+    const RowOut& out = w ? g.out0 : g.out1;
+    __nv_bfloat16* dst = out.p + (size_t(it.s.k0) + b) * out.row + hk * out.head;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32)
+      store_row32(tmem + lane_base + 256 + w * 128 + c0, ok && n > 0, b < it.s.nk,
+                  w ? g.scale : 1.f, dst + c0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_free(tmem, 512);
 }
 
 RowView view(const void* p, const sla_strides& s) {
@@ -126,50 +656,64 @@ RowView view(const void* p, const sla_strides& s) {
 }
 RowOut out(void* p, const sla_strides& s) { return {static_cast<__nv_bfloat16*>(p), s.row, s.head}; }
 
+template <typename K>
+cudaError_t launch(K* kernel, int smem, unsigned grid, const CUtensorMap& tq,
+                   const CUtensorMap& tdo, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const CbArgs& a, cudaStream_t s) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, smem, s>>>(tq, tdo, tk, tv, a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-cudaError_t launch_causal_dvec(const CausalProblem& p, const ItemList& list, const void* o,
-                               const void* d_o, float* dvec, cudaStream_t s) {
-  const dim3 grid(list.most, p.Hq);
+cudaError_t launch_causal_dvec(const CausalProblem& p, const void* o, const void* d_o, float* dvec,
+                               cudaStream_t s) {
+  const long long n = (long long)p.total_q * p.Hq;
+  const int per = 256 / (p.d / 8);
+  const unsigned grid = unsigned((n + per - 1) / per);
   if (p.d == 128)
-    causal_dvec_kernel<128><<<grid, kWarps * 32, 0, s>>>(view(o, p.o), view(d_o, p.o), list.count, list.items, dvec,
-                                                         p.total_q);
+    causal_dvec_kernel<128><<<grid, 256, 0, s>>>(view(o, p.o), view(d_o, p.o), dvec, p.total_q,
+                                                 p.Hq);
   else
-    causal_dvec_kernel<64><<<grid, kWarps * 32, 0, s>>>(view(o, p.o), view(d_o, p.o), list.count, list.items, dvec,
-                                                        p.total_q);
+    causal_dvec_kernel<64><<<grid, 256, 0, s>>>(view(o, p.o), view(d_o, p.o), dvec, p.total_q,
+                                                p.Hq);
   return cudaGetLastError();
 }
 
 cudaError_t launch_causal_dq(const CausalProblem& p, const void* q, const void* k, const void* v,
-                             const ItemList& list, const void* d_o, const float* lse, const float* dvec,
-                             void* dq, int* err, cudaStream_t s) {
-  (void)err;
-  const dim3 grid(list.most, p.Hq);
-  if (p.d == 128)
-    causal_dq_kernel<128><<<grid, kWarps * 32, 0, s>>>(view(q, p.q), view(k, p.k), view(v, p.v),
-                                                       view(d_o, p.o), list.count, list.items, lse, dvec,
-                                                       out(dq, p.q), p.total_q, p.G, p.scale);
-  else
-    causal_dq_kernel<64><<<grid, kWarps * 32, 0, s>>>(view(q, p.q), view(k, p.k), view(v, p.v),
-                                                      view(d_o, p.o), list.count, list.items, lse, dvec,
-                                                      out(dq, p.q), p.total_q, p.G, p.scale);
-  return cudaGetLastError();
+                             const ItemList& list, const void* d_o, const float* lse,
+                             const float* dvec, void* dq, int* err, cudaStream_t s) {
+  CUtensorMap tq, tdo, tk, tv;
+  if (!make_tmap_rows(&tq, q, p.total_q, p.Hq, p.d, p.q, 128) ||
+      !make_tmap_rows(&tdo, d_o, p.total_q, p.Hq, p.d, p.o, 128) ||
+      !make_tmap_rows(&tk, k, p.total_k, p.Hkv, p.d, p.k, 64) ||
+      !make_tmap_rows(&tv, v, p.total_k, p.Hkv, p.d, p.v, 64))
+    return cudaErrorInvalidValue;
+  const int heads = pair_heads(p) ? p.Hq / 2 : p.Hq;
+  const CbArgs a{list.count, list.items, lse,   dvec, out(dq, p.q), RowOut{}, p.total_q,
+                 heads,      p.G,        pair_heads(p), p.scale, p.scale_log2, err};
+  const unsigned grid = unsigned(list.most) * heads;
+  return p.d == 128 ? launch(causal_dq_kernel<128>, kDqTotal<128>, grid, tq, tdo, tk, tv, a, s)
+                    : launch(causal_dq_kernel<64>, kDqTotal<64>, grid, tq, tdo, tk, tv, a, s);
 }
 
 cudaError_t launch_causal_dkv(const CausalProblem& p, const void* q, const void* k, const void* v,
                               const ItemList& list, const void* d_o, const float* lse,
                               const float* dvec, void* dk, void* dv, int* err, cudaStream_t s) {
-  (void)err;
-  const dim3 grid(list.most, p.Hkv);
-  if (p.d == 128)
-    causal_dkv_kernel<128><<<grid, kWarps * 32, 0, s>>>(
-        view(q, p.q), view(k, p.k), view(v, p.v), view(d_o, p.o), list.count, list.items, lse, dvec, out(dk, p.k),
-        out(dv, p.v), p.total_q, p.G, p.scale);
-  else
-    causal_dkv_kernel<64><<<grid, kWarps * 32, 0, s>>>(
-        view(q, p.q), view(k, p.k), view(v, p.v), view(d_o, p.o), list.count, list.items, lse, dvec, out(dk, p.k),
-        out(dv, p.v), p.total_q, p.G, p.scale);
-  return cudaGetLastError();
+  CUtensorMap tq, tdo, tk, tv;
+  if (!make_tmap_rows(&tq, q, p.total_q, p.Hq, p.d, p.q, 128) ||
+      !make_tmap_rows(&tdo, d_o, p.total_q, p.Hq, p.d, p.o, 128) ||
+      !make_tmap_rows(&tk, k, p.total_k, p.Hkv, p.d, p.k, 128) ||
+      !make_tmap_rows(&tv, v, p.total_k, p.Hkv, p.d, p.v, 128))
+    return cudaErrorInvalidValue;
+  const CbArgs a{list.count, list.items, lse,   dvec,    out(dk, p.k), out(dv, p.v), p.total_q,
+                 p.Hkv,      p.G,        false, p.scale, p.scale_log2, err};
+  const unsigned grid = unsigned(list.most) * p.Hkv;
+  return p.d == 128 ? launch(causal_dkv_kernel<128>, kDkTotal<128>, grid, tq, tdo, tk, tv, a, s)
+                    : launch(causal_dkv_kernel<64>, kDkTotal<64>, grid, tq, tdo, tk, tv, a, s);
 }
 
 }  // namespace sla

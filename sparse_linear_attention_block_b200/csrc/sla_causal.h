@@ -68,17 +68,48 @@ struct DecayProblem {
   sla_strides q, k, v, o;
 };
 
+// A piece of a sequence that one CTA (per head) walks: `rows` rows from `row` on.
+// slot: where its state is kept between the kernels, -1 if the piece is a whole
+// sequence.  first, last: whether it is the sequence's.
+struct alignas(16) Piece {
+  int row, rows, seq, slot;
+  int first, last, pad0, pad1;
+};
+// A sequence of several pieces: their slots are slot .. slot + pieces - 1.
+struct alignas(16) Split {
+  int seq, slot, pieces, last_rows;
+};
+
+// How the sequences are cut: pieces of `rows` rows.  Sequences of one piece and
+// sequences of several have lists of their own.
+struct DecayCut {
+  int rows;
+  int most_slots;   // pieces of cut sequences: below 2 total / rows
+  int most_splits;  // cut sequences: below total / rows
+};
+
 struct DecayLayout {
   size_t err;
-  size_t seqs;  // Seq [n_seq] (k0, nk unused)
+  size_t counts;  // int [4]: slots, splits, whole sequences
+  size_t pieces;  // Piece [most_slots + n_seq]: pieces of cut sequences, then whole ones
+  size_t splits;  // Split [most_splits]
+  size_t states;  // fp32 [most_slots][H][d][d]
   size_t total;
+};
+
+struct DecayLists {
+  int* counts;
+  Piece* pieces;
+  Split* splits;
+  float* states;
 };
 
 // What a plan makes: the list of query tiles and, for a backward, of key tiles.
 struct CausalPlan {
-  int q_tile;
+  int q_tile, q_most;
   Item* q_items;
   int* q_count;
+  int k_most;
   Item* k_items;  // may be null
   int* k_count;
 };
@@ -104,6 +135,10 @@ inline bool make_tmap_rows(CUtensorMap* m, const void* base, int rows, int heads
                            uint64_t(st.row), uint64_t(st.head), 64, uint32_t(box_rows));
 }
 
+// CTAs that a decay kernel keeps running at once: two on each SM.
+constexpr int kDecaySlots = 296;
+constexpr int kDecayChunk = 64;
+
 // One recurrence R over a sequence's tokens, in order or from the last to the
 // first, and what is read from it:
 //   forward:  R = l R + y_t z_t^T,        out_t = fs_out R^T x_t
@@ -117,10 +152,19 @@ struct DecayRun {
   float* state_out;
   bool reverse, state_t;
 };
-cudaError_t launch_decay_plan(const DecayProblem& p, const int32_t* off, const float* log_decay,
-                              Seq* seqs, int* err, cudaStream_t s);
-cudaError_t launch_decay_run(const DecayProblem& p, const DecayRun& r, const Seq* seqs,
-                             const float* log_decay, int* err, cudaStream_t s);
+cudaError_t launch_decay_plan(const DecayProblem& p, const DecayCut& cut, const int32_t* off,
+                              const float* log_decay, const DecayLists& l, int* err,
+                              cudaStream_t s);
+// The states before each piece of the cut sequences, into their slots: every
+// piece's own sum, then a walk over the pieces.
+cudaError_t launch_decay_pieces(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+                                const DecayLists& l, const float* log_decay, int* err,
+                                cudaStream_t s);
+cudaError_t launch_decay_scan(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+                              const DecayLists& l, const float* log_decay, cudaStream_t s);
+cudaError_t launch_decay_run(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+                             const DecayLists& l, const float* log_decay, int* err,
+                             cudaStream_t s);
 cudaError_t launch_decay_step(const DecayProblem& p, const void* q, const void* k, const void* v,
                               const float* log_decay, const float* state_in, float* state_out,
                               void* o, cudaStream_t s);

@@ -81,6 +81,8 @@ sla_status check_decay(const sla_decay_shape* s, DecayProblem* p) {
   if (!resolve(s->q, s->total, s->H, s->d, &p->q) || !resolve(s->k, s->total, s->H, s->d, &p->k) ||
       !resolve(s->v, s->total, s->H, s->d, &p->v) || !resolve(s->o, s->total, s->H, s->d, &p->o))
     return SLA_ERR_INVALID_ARG;
+  // grids: one CTA for each piece (of at least 256 rows) or sequence, and head
+  if ((size_t(p->total) / 128 + p->n_seq) * p->H >= (1u << 31)) return SLA_ERR_UNSUPPORTED;
   return SLA_OK;
 }
 
@@ -105,13 +107,38 @@ CausalLayout causal_layout(const CausalProblem& p) {
   return L;
 }
 
-DecayLayout decay_layout(const DecayProblem& p) {
+// Pieces as long as keep every CTA slot of the GPU busy with one, whole chunks, and not
+// below 256 rows: a shorter piece costs more in its state (as many bytes as 128 rows of
+// q, k, v and o) than it gains.
+DecayCut decay_cut(const DecayProblem& p) {
+  const long long even = ((long long)p.total * p.H + kDecaySlots - 1) / kDecaySlots;
+  const long long rows = (even + kDecayChunk - 1) / kDecayChunk * kDecayChunk;
+  DecayCut c{};
+  c.rows = int(rows < 256 ? 256 : rows > kMaxRows ? kMaxRows : rows);
+  if (p.total > c.rows) {
+    // a cut sequence has n >= 2 pieces and more than (n - 1) rows of them
+    c.most_slots = int(2ll * p.total / c.rows);
+    c.most_splits = p.total / c.rows;
+  }
+  return c;
+}
+
+DecayLayout decay_layout(const DecayProblem& p, const DecayCut& c) {
   Taker take;
   DecayLayout L{};
   L.err = take(256);
-  L.seqs = take(size_t(p.n_seq) * sizeof(Seq));
+  L.counts = take(4 * sizeof(int));
+  L.pieces = take((size_t(c.most_slots) + p.n_seq) * sizeof(Piece));
+  L.splits = take(size_t(c.most_splits) * sizeof(Split));
+  L.states = take(size_t(c.most_slots) * p.H * p.d * p.d * 4);
   L.total = take.off;
   return L;
+}
+
+DecayLists decay_lists(void* ws, const DecayLayout& L) {
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  return {reinterpret_cast<int*>(b + L.counts), reinterpret_cast<Piece*>(b + L.pieces),
+          reinterpret_cast<Split*>(b + L.splits), reinterpret_cast<float*>(b + L.states)};
 }
 
 sla_status check_workspace(const void* ws, size_t bytes, size_t need) {
@@ -136,6 +163,17 @@ RowOut out_view(void* p, const sla_strides& s) {
     if (launch_named(name, stream, [&] { return (expr); }) != cudaSuccess) \
       return SLA_ERR_CUDA;                                                 \
   } while (0)
+
+// One output: the states before the pieces of cut sequences, then the walk.
+sla_status decay_pass(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+                      const DecayLists& l, const float* log_decay, int* err, cudaStream_t s) {
+  if (cut.most_slots > 0) {
+    SLA_LAUNCH("decay_pieces", s, launch_decay_pieces(p, cut, r, l, log_decay, err, s));
+    SLA_LAUNCH("decay_scan", s, launch_decay_scan(p, cut, r, l, log_decay, s));
+  }
+  SLA_LAUNCH("decay_run", s, launch_decay_run(p, cut, r, l, log_decay, err, s));
+  return SLA_OK;
+}
 
 }  // namespace
 
@@ -167,9 +205,10 @@ sla_status sla_causal_forward(const sla_causal_shape* shape, const void* q, cons
   int* err = at<int>(workspace, L.err);
   int* counts = at<int>(workspace, L.counts);
   Item* items = at<Item>(workspace, L.items);
-  const CausalPlan plan{fwd_tile(p), items, counts, nullptr, nullptr};
+  const int most = int(most_items(p.total_q, fwd_tile(p), p.n_seq));
+  const CausalPlan plan{fwd_tile(p), most, items, counts, 0, nullptr, nullptr};
   SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, k_len, plan, err, s));
-  const ItemList list{counts, items, int(most_items(p.total_q, plan.q_tile, p.n_seq))};
+  const ItemList list{counts, items, most};
   SLA_LAUNCH("causal_fwd", s, launch_causal_fwd(p, q, k, v, list, o, lse, err, s));
   return SLA_OK;
 }
@@ -192,10 +231,12 @@ sla_status sla_causal_backward(const sla_causal_shape* shape, const void* q, con
   int* counts = at<int>(workspace, L.counts);
   Item *items = at<Item>(workspace, L.items), *kitems = at<Item>(workspace, L.kitems);
   float* dvec = at<float>(workspace, L.dvec);
-  const CausalPlan plan{fwd_tile(p), items, counts, kitems, counts + 1};
+  const int most = int(most_items(p.total_q, fwd_tile(p), p.n_seq)),
+            kmost = int(most_items(p.total_k, kRowTile, p.n_seq));
+  const CausalPlan plan{fwd_tile(p), most, items, counts, kmost, kitems, counts + 1};
   SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, nullptr, plan, err, s));
-  const ItemList list{counts, items, int(most_items(p.total_q, plan.q_tile, p.n_seq))};
-  const ItemList klist{counts + 1, kitems, int(most_items(p.total_k, kRowTile, p.n_seq))};
+  const ItemList list{counts, items, most};
+  const ItemList klist{counts + 1, kitems, kmost};
   SLA_LAUNCH("causal_dvec", s, launch_causal_dvec(p, o, d_o, dvec, s));
   SLA_LAUNCH("causal_dkv", s,
              launch_causal_dkv(p, q, k, v, klist, d_o, lse, dvec, dk, dv, err, s));
@@ -209,7 +250,7 @@ sla_status sla_decay_query_sizes(const sla_decay_shape* shape, sla_decay_sizes* 
   const sla_status st = check_decay(shape, &p);
   if (st != SLA_OK) return st;
   out->state_bytes = size_t(p.n_seq) * p.H * p.d * p.d * 4;
-  out->workspace_bytes = decay_layout(p).total;
+  out->workspace_bytes = decay_layout(p, decay_cut(p)).total;
   return SLA_OK;
 }
 
@@ -223,16 +264,16 @@ sla_status sla_decay_forward(const sla_decay_shape* shape, const void* q, const 
   if (!good(q) || !good(k) || !good(v) || !good(o) || !log_decay || !aligned(log_decay, 4) ||
       !off || !aligned(off, 4) || !good_or_null(state_in) || !good_or_null(state_out))
     return SLA_ERR_INVALID_ARG;
-  const DecayLayout L = decay_layout(p);
+  const DecayCut cut = decay_cut(p);
+  const DecayLayout L = decay_layout(p, cut);
   if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = at<int>(workspace, L.err);
-  Seq* seqs = at<Seq>(workspace, L.seqs);
-  SLA_LAUNCH("decay_plan", s, launch_decay_plan(p, off, log_decay, seqs, err, s));
+  const DecayLists l = decay_lists(workspace, L);
+  SLA_LAUNCH("decay_plan", s, launch_decay_plan(p, cut, off, log_decay, l, err, s));
   const DecayRun r{view(q, p.q), view(k, p.k), view(v, p.v), out_view(o, p.o),
                    state_in,     state_out,    false,        false};
-  SLA_LAUNCH("decay_fwd", s, launch_decay_run(p, r, seqs, log_decay, err, s));
-  return SLA_OK;
+  return decay_pass(p, cut, r, l, log_decay, err, s);
 }
 
 sla_status sla_decay_backward(const sla_decay_shape* shape, const void* q, const void* k,
@@ -247,21 +288,21 @@ sla_status sla_decay_backward(const sla_decay_shape* shape, const void* q, const
       !log_decay || !aligned(log_decay, 4) || !off || !aligned(off, 4) ||
       !good_or_null(state_in) || !good_or_null(d_state_out) || !good_or_null(d_state_in))
     return SLA_ERR_INVALID_ARG;
-  const DecayLayout L = decay_layout(p);
+  const DecayCut cut = decay_cut(p);
+  const DecayLayout L = decay_layout(p, cut);
   if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = at<int>(workspace, L.err);
-  Seq* seqs = at<Seq>(workspace, L.seqs);
-  SLA_LAUNCH("decay_plan", s, launch_decay_plan(p, off, log_decay, seqs, err, s));
+  const DecayLists l = decay_lists(workspace, L);
+  SLA_LAUNCH("decay_plan", s, launch_decay_plan(p, cut, off, log_decay, l, err, s));
   const RowView vq = view(q, p.q), vk = view(k, p.k), vv = view(v, p.v), vd = view(d_o, p.o);
   const DecayRun rq{vd, vv, vk, out_view(dq, p.q), state_in, nullptr, false, true};
   const DecayRun rk{vv, vd, vq, out_view(dk, p.k), d_state_out, nullptr, true, true};
   // last: d_state_in may be d_state_out's buffer
   const DecayRun rv{vk, vq, vd, out_view(dv, p.v), d_state_out, d_state_in, true, false};
-  SLA_LAUNCH("decay_dq", s, launch_decay_run(p, rq, seqs, log_decay, err, s));
-  SLA_LAUNCH("decay_dk", s, launch_decay_run(p, rk, seqs, log_decay, err, s));
-  SLA_LAUNCH("decay_dv", s, launch_decay_run(p, rv, seqs, log_decay, err, s));
-  return SLA_OK;
+  if ((st = decay_pass(p, cut, rq, l, log_decay, err, s)) != SLA_OK) return st;
+  if ((st = decay_pass(p, cut, rk, l, log_decay, err, s)) != SLA_OK) return st;
+  return decay_pass(p, cut, rv, l, log_decay, err, s);
 }
 
 sla_status sla_decay_step(const sla_decay_shape* shape, const void* q, const void* k,

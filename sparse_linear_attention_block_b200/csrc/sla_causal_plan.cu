@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(kPlanThreads) causal_plan_kernel(PlanIn in, Ca
   const bool keys = blockIdx.x == 1;
   const int tile = keys ? kRowTile : plan.q_tile;
   Item* items = keys ? plan.k_items : plan.q_items;
+  const int most = keys ? plan.k_most : plan.q_most;
   const int t = threadIdx.x, warp = t / 32, lane = t % 32;
   for (int b = t; b < kBuckets; b += kPlanThreads) hist[b] = 0;
   __syncthreads();
@@ -75,7 +76,12 @@ __global__ void __launch_bounds__(kPlanThreads) causal_plan_kernel(PlanIn in, Ca
       if (lane >= o) w += x;
     }
     warp_sum[lane] = w;
-    if (lane == 31) *(keys ? plan.k_count : plan.q_count) = w;
+    if (lane == 31) {
+      // sequences that overlap (offsets that fall back) could have more tiles than there is
+      // room for: what is beyond is left out and reported
+      if (w > most) set_error(err, SLA_ERR_DEVICE);
+      *(keys ? plan.k_count : plan.q_count) = min(w, most);
+    }
   }
   __syncthreads();
   const int before = sum - a - b + (warp > 0 ? warp_sum[warp - 1] : 0);
@@ -87,22 +93,61 @@ __global__ void __launch_bounds__(kPlanThreads) causal_plan_kernel(PlanIn in, Ca
     const int n = ((keys ? s.nk : s.nq) + tile - 1) / tile;
     for (int j = lane; j < n; j += 32) {
       const int at = atomicAdd(&hist[bucket(item_cost(s, j, tile, keys))], 1);
-      items[at] = Item{s, j, i, 0, 0};
+      if (at < most) items[at] = Item{s, j, i, 0, 0};
     }
   }
 }
 
-__global__ void decay_plan_kernel(const int32_t* __restrict__ off,
-                                  const float* __restrict__ log_decay, int n_seq, int total, int H,
-                                  Seq* __restrict__ seqs, int* err) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < H && !(log_decay[i] <= 0.f)) set_error(err, SLA_ERR_DEVICE);
-  if (i >= n_seq) return;
-  const int a = off[i], b = off[i + 1];
-  const bool ok = a >= 0 && b >= a && b <= total;
-  if (!ok) set_error(err, SLA_ERR_DEVICE);
-  // -1 marks a bad sequence: nothing of it is written, not even its state
-  seqs[i] = ok ? Seq{a, b - a, 0, 0} : Seq{0, -1, 0, 0};
+// One CTA: every sequence is checked and cut into pieces of cut.rows rows.  The
+// places in the lists are handed out by counters in shared memory; no result
+// depends on them.
+__global__ void __launch_bounds__(kPlanThreads) decay_plan_kernel(
+    const int32_t* __restrict__ off, const float* __restrict__ log_decay, int n_seq, int total,
+    int H, DecayCut cut, DecayLists l, int* err) {
+  __shared__ int slots, splits, whole, end;
+  if (threadIdx.x == 0) slots = splits = whole = end = 0;
+  __syncthreads();
+  for (int h = threadIdx.x; h < H; h += kPlanThreads)
+    if (!(log_decay[h] <= 0.f)) set_error(err, SLA_ERR_DEVICE);
+  const int lane = threadIdx.x % 32;
+  for (int i = threadIdx.x / 32; i < n_seq; i += kPlanThreads / 32) {
+    const int a = off[i], b = off[i + 1];
+    if (a < 0 || b < a || b > total) {
+      // nothing of a bad sequence is written, not even its state
+      if (lane == 0) set_error(err, SLA_ERR_DEVICE);
+      continue;
+    }
+    const int n = (b - a + cut.rows - 1) / cut.rows;
+    if (n <= 1) {
+      if (lane == 0)
+        l.pieces[cut.most_slots + atomicAdd(&whole, 1)] = Piece{a, b - a, i, -1, 1, 1, 0, 0};
+      continue;
+    }
+    int at = 0;
+    if (lane == 0) {
+      at = atomicAdd(&slots, n);
+      // overlapping sequences (offsets that fall back) could ask for more than there is
+      // (those that fit have the lowest places: what follows one that does not, does not)
+      if (at + n <= cut.most_slots) {
+        atomicMax(&end, at + n);
+        l.splits[atomicAdd(&splits, 1)] = Split{i, at, n, b - a - (n - 1) * cut.rows};
+      }
+    }
+    at = __shfl_sync(0xffffffffu, at, 0);
+    if (at + n > cut.most_slots) {
+      if (lane == 0) set_error(err, SLA_ERR_DEVICE);
+      continue;
+    }
+    for (int j = lane; j < n; j += 32)
+      l.pieces[at + j] = Piece{a + j * cut.rows, min(cut.rows, b - a - j * cut.rows), i, at + j,
+                               j == 0, j == n - 1, 0, 0};
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    l.counts[0] = end;
+    l.counts[1] = splits;
+    l.counts[2] = whole;
+  }
 }
 
 }  // namespace
@@ -118,11 +163,10 @@ cudaError_t launch_causal_plan(const CausalProblem& p, const int32_t* q_off, con
   return cudaGetLastError();
 }
 
-cudaError_t launch_decay_plan(const DecayProblem& p, const int32_t* off, const float* log_decay,
-                              Seq* seqs, int* err, cudaStream_t s) {
-  const int n = p.n_seq > p.H ? p.n_seq : p.H;
-  decay_plan_kernel<<<(n + 255) / 256, 256, 0, s>>>(off, log_decay, p.n_seq, p.total, p.H, seqs,
-                                                    err);
+cudaError_t launch_decay_plan(const DecayProblem& p, const DecayCut& cut, const int32_t* off,
+                              const float* log_decay, const DecayLists& l, int* err,
+                              cudaStream_t s) {
+  decay_plan_kernel<<<1, kPlanThreads, 0, s>>>(off, log_decay, p.n_seq, p.total, p.H, cut, l, err);
   return cudaGetLastError();
 }
 

@@ -14,42 +14,379 @@
 namespace sla {
 namespace {
 
-// One CTA per (sequence, head), one thread per column of the state (fp32).
+// Design of a run (sm_100a).  A CTA (256 threads, two CTAs per SM) walks a piece
+// of a sequence in chunks of 64 tokens with the state as S^T [z][y] in TMEM
+// (fp32).  Per chunk of r tokens, w_n = l^n, forward (reversed runs mirror the
+// exponents):
+//   A[s][t]  = y_s . x_t                          MMA, tokens s on the lanes
+//   P[s][t]  = w_{t-s} A[s][t]  (s <= t)          bf16, to shared memory
+//   O1[z][t] = sum_y S[z][y] x_t[y]               MMA, S rounded to bf16 in TMEM
+//   O2[z][t] = sum_s z_s P[s][t]                  MMA
+//   out_t    = w_{t+1} O1[.][t] + O2[.][t]
+//   S        = w_r S + sum_s z_s (w_{r-1-s} y_s)^T   MMA on top of w_r S
+// The state is held to 32 bits: w y is fed as three bf16 numbers (their sum has
+// 24 bits) and w_r S is a product with a two-number factor; only what a query
+// reads (S and P as operands) is rounded to bf16, like the output.
+// The features lie on the TMEM lanes everywhere (M = 128, for d = 64 with lanes
+// that nobody reads), so the state goes from its accumulator to an A operand
+// without leaving its lanes.  TMEM: S at 0, A then S (bf16) then O2 at 128, O1
+// at 192: 256 columns.
+// The bytes of a chunk (x, y, z, out) take longer than its products; what is
+// to be hidden is the chain state -> S in bf16 -> products -> state, which two
+// CTAs per SM do for one another.
 template <int D>
-__global__ void __launch_bounds__(D) decay_run_kernel(DecayRun r, const Seq* __restrict__ seqs,
-                                                      const float* __restrict__ log_decay, int H,
-                                                      float fs_out, float fs_up) {
-  __shared__ float sx[D], sy[D];
-  const Seq sq = seqs[blockIdx.x];
-  if (sq.nq < 0) return;
-  const int h = blockIdx.y, z = threadIdx.x;
-  const Factor l = decay_factor(decay_checked(log_decay[h]), 1);
-  float S[D];
-  const size_t base = (size_t(blockIdx.x) * H + h) * D * D;
-#pragma unroll
-  for (int y = 0; y < D; ++y)
-    S[y] = r.state_in ? r.state_in[base + (r.state_t ? z * D + y : y * D + z)] : 0.f;
-  for (int i = 0; i < sq.nq; ++i) {
-    const size_t row = size_t(sq.q0) + (r.reverse ? sq.nq - 1 - i : i);
-    sx[z] = __bfloat162float(r.x.p[row * r.x.row + h * r.x.head + z]);
-    sy[z] = __bfloat162float(r.y.p[row * r.y.row + h * r.y.head + z]) * fs_up;
-    const float zz = __bfloat162float(r.z.p[row * r.z.row + h * r.z.head + z]);
-    __syncthreads();
-    float acc = 0.f;
-#pragma unroll
-    for (int y = 0; y < D; ++y) {
-      if (!r.reverse) S[y] = scaled(S[y], l);
-      S[y] = fmaf(sy[y], zz, S[y]);
-      acc = fmaf(sx[y], S[y], acc);
-      if (r.reverse) S[y] = scaled(S[y], l);
-    }
-    r.out.p[row * r.out.row + h * r.out.head + z] = __float2bfloat16(acc * fs_out);
-    __syncthreads();
+struct DrSmem {
+  static constexpr int kT = 64 * D * 2;                      // x, y or z of a chunk
+  static constexpr int kX = 0, kY = kT, kZ = 2 * kT, kP = 3 * kT, kYs = kP + 8192;
+  static constexpr int kPow = kYs + 3 * kT;                  // w_0 .. w_64
+  static constexpr int kBars = kPow + 272;
+  // no more than two CTAs per SM: each takes half of TMEM
+  static constexpr int kTotal = kBars + 128 > 80 * 1024 ? kBars + 128 : 80 * 1024;
+};
+struct DrBars {
+  uint64_t x_full, y_full, z_full, a_done, o_done, u_done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+struct DrArgs {
+  const int* counts;
+  const Piece* pieces;
+  float* states;
+  const float* log_decay;
+  DecayRun r;
+  int H, most_slots;
+  float f_intra, f_inter, f_up;
+  int* err;
+};
+
+// kStateOnly: the piece's own sum (from a zero state) into its slot, no output.
+template <int D, bool kStateOnly>
+__global__ void __launch_bounds__(256, 2) decay_run_kernel(
+    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
+    const __grid_constant__ CUtensorMap tm_z, const DrArgs g) {
+  using L = DrSmem<D>;
+  constexpr int kHalf = D / 2;  // state columns of a warpgroup
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int idx = blockIdx.x / g.H, h = blockIdx.x % g.H;
+  if (kStateOnly ? idx >= g.counts[0]
+                 : !(idx < g.counts[0] ||
+                     (idx >= g.most_slots && idx - g.most_slots < g.counts[2])))
+    return;
+  const Piece pc = g.pieces[idx];
+  const bool rev = g.r.reverse;
+  // the walk over the pieces does not need the last one's sum
+  if (kStateOnly && (rev ? pc.first : pc.last)) return;
+  if ((smem_u32(smem) & 1023u) != 0u) {
+    if (threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
+    return;
   }
-  if (r.state_out) {
+  float* pw = reinterpret_cast<float*>(smem + L::kPow);
+  DrBars& bb = *reinterpret_cast<DrBars*>(smem + L::kBars);
+  int* err = g.err;
+  volatile int* abort_flag = &bb.abort_flag;
+  const int t = threadIdx.x, warp = t / 32, lane = t % 32;
+  const int wg = warp >> 2, z = (warp & 3) * 32 + lane;  // TMEM lane
+  const float gl = decay_checked(g.log_decay[h]);
+
+  if (warp == 0) tmem_alloc(&bb.tmem_base, 256);
+  if (t == 32) {
+    mbar_init(&bb.x_full, 1);
+    mbar_init(&bb.y_full, 1);
+    mbar_init(&bb.z_full, 1);
+    mbar_init(&bb.a_done, 1);
+    mbar_init(&bb.o_done, 1);
+    mbar_init(&bb.u_done, 1);
+    bb.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (t >= 64 && t < 64 + 65) pw[t - 64] = decay_factor(gl, t - 64).hi;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bb.tmem_base;
+  const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+  const uint32_t tS = tmem + lane_base + wg * kHalf, tA = tmem + lane_base + 128,
+                 tO1 = tmem + lane_base + 192;
+  const int chunks = (pc.rows + 63) / 64;
+  // rows of the c-th chunk in walking order
+  auto chunk_row = [&](int c) { return (rev ? chunks - 1 - c : c) * 64; };
+  auto load = [&](const CUtensorMap& tm, int at, uint64_t* bar, int c) {  // one thread
+    mbar_arrive_expect_tx(bar, L::kT);
 #pragma unroll
-    for (int y = 0; y < D; ++y)
-      r.state_out[base + (r.state_t ? z * D + y : y * D + z)] = S[y];
+    for (int k = 0; k < D / 64; ++k)
+      tma_load_3d(smem + at + k * 8192, bar, &tm, k * 64, pc.row + chunk_row(c), h);
+  };
+  if (t == 0 && chunks > 0) {
+    load(tm_y, L::kY, &bb.y_full, 0);
+    if (!kStateOnly) load(tm_x, L::kX, &bb.x_full, 0);
+    load(tm_z, L::kZ, &bb.z_full, 0);
+  }
+
+  // the state before the piece
+  {
+    const size_t dd = size_t(D) * D;
+    const float* src = nullptr;
+    bool turned = false;
+    if (!kStateOnly) {
+      if (pc.slot >= 0) {
+        src = g.states + (size_t(pc.slot) * g.H + h) * dd;
+      } else if (g.r.state_in) {
+        src = g.r.state_in + (size_t(pc.seq) * g.H + h) * dd;
+        turned = g.r.state_t;
+      }
+    }
+#pragma unroll 1
+    for (int c0 = 0; c0 < kHalf; c0 += 16) {
+      uint32_t w[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int y = wg * kHalf + c0 + e;
+        w[e] = src && z < D ? __float_as_uint(src[turned ? z * D + y : y * D + z]) : 0u;
+      }
+      tmem_st16(tS + c0, w);
+    }
+    tmem_st_wait();
+  }
+  const Factor whole = decay_factor(gl, 64);
+  bool ok = true;
+
+  for (int c = 0; c < chunks; ++c) {
+    const int row0 = chunk_row(c), r = min(64, pc.rows - row0);
+    const uint32_t ph = c & 1;
+    const Factor carry = r < 64 ? decay_factor(gl, r) : whole;
+    ok = mbar_wait(&bb.y_full, ph, err, abort_flag) && ok;
+    if (!kStateOnly && t == 0 && ok && (ok = mbar_wait(&bb.x_full, ph, err, abort_flag))) {
+      constexpr uint32_t id_a = idesc_bf16(128, 64, 0, 0);
+      const uint64_t yd = desc_kmajor_base(smem_u32(smem + L::kY)),
+                     xd = desc_kmajor_base(smem_u32(smem + L::kX));
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        mma_ss(tmem + 128, desc_advance(yd, kmajor_step_bytes(64, ks)),
+               desc_advance(xd, kmajor_step_bytes(64, ks)), id_a, ks > 0);
+      mma_commit(&bb.a_done);
+    }
+    if (ok) {
+      // w y in three bf16 parts; rows behind the piece are 0
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int e = t + i * 256, s = e / (D / 8), col = (e % (D / 8)) * 8;
+        const uint32_t at = (col >> 6) * 8192 + sw128_offset(s, col & 63);
+        const uint4 u = *reinterpret_cast<const uint4*>(smem + L::kY + at);
+        const float f = s < r ? g.f_up * pw[rev ? s + 1 : r - 1 - s] : 0.f;
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t p0[4], p1[4], p2[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float a = s < r ? bf16_lo(w[k]) * f : 0.f, b = s < r ? bf16_hi(w[k]) * f : 0.f;
+          p0[k] = pack_bf16(a, b);
+          a -= bf16_lo(p0[k]);
+          b -= bf16_hi(p0[k]);
+          p1[k] = pack_bf16(a, b);
+          p2[k] = pack_bf16(a - bf16_lo(p1[k]), b - bf16_hi(p1[k]));
+        }
+        uint8_t* dst = smem + L::kYs + at;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(p0[0], p0[1], p0[2], p0[3]);
+        *reinterpret_cast<uint4*>(dst + L::kT) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+        *reinterpret_cast<uint4*>(dst + 2 * L::kT) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+      }
+    }
+    // the state: rounded for the products, decayed for the sum
+    uint32_t sb[kHalf / 2];
+#pragma unroll
+    for (int c0 = 0; c0 < kHalf; c0 += 32) {
+      float v[32];
+      tmem_ld32(tS + c0, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sb[c0 / 2 + e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(scaled(v[q * 16 + e], carry));
+        tmem_st16(tS + c0 + q * 16, w);
+      }
+    }
+    if (!kStateOnly) {
+      ok = ok && mbar_wait(&bb.a_done, ph, err, abort_flag);
+      tc_fence_after();
+      if (ok) {
+        // a warp reads A and writes S in the same 32 columns of its own lanes
+        if ((warp & 3) < 2) {
+          const int s = z;
+          float v[32];
+          tmem_ld32(tA + wg * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float f[2];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int e = u * 8 + k * 2 + q, n = rev ? s - (wg * 32 + e) : wg * 32 + e - s;
+                f[q] = n >= 0 && s < r ? v[e] * (g.f_intra * pw[n < 0 ? 0 : n]) : 0.f;
+              }
+              p[k] = pack_bf16(f[0], f[1]);
+            }
+            st_sw128_unit(smem + L::kP, 64, s, wg * 32 + u * 8, make_uint4(p[0], p[1], p[2], p[3]));
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kHalf / 2; q += 16) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = sb[q + e];
+          tmem_st16(tA + wg * 32 + q, w);
+        }
+      }
+    }
+    if (r < 64 && ok && (ok = mbar_wait(&bb.z_full, ph, err, abort_flag))) {
+      // the rows of z behind the piece belong to others: 0 times NaN would be NaN
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k)
+        for (int b = r * 128 + t * 16; b < 8192; b += 4096)
+          *reinterpret_cast<uint4*>(smem + L::kZ + k * 8192 + b) = make_uint4(0, 0, 0, 0);
+    }
+    tmem_st_wait();
+    fence_proxy_async_smem();
+    tc_fence_before();
+    ok = __syncthreads_and(ok);
+    tc_fence_after();
+    if (!ok) break;
+    if (t == 0) {
+      const bool more = c + 1 < chunks;
+      if (more) load(tm_y, L::kY, &bb.y_full, c + 1);
+      constexpr uint32_t id_o1 = idesc_bf16(128, 64, 0, 0), id_o2 = idesc_bf16(128, 64, 1, 1),
+                         id_u = idesc_bf16(128, D, 1, 1);
+      const uint64_t zd = desc_mnmajor_base(smem_u32(smem + L::kZ), 64);
+      if (!kStateOnly) {
+        const uint64_t xd = desc_kmajor_base(smem_u32(smem + L::kX)),
+                       pd = desc_mnmajor_base(smem_u32(smem + L::kP), 64);
+        constexpr int kPer = D / 32;  // k-steps of a warpgroup's half of the state
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ts(tmem + 192, tmem + 128 + (ks / kPer) * 32 + (ks % kPer) * 8,
+                 desc_advance(xd, kmajor_step_bytes(64, ks)), id_o1, ks > 0);
+        ok = mbar_wait(&bb.z_full, ph, err, abort_flag);
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ss(tmem + 128, desc_advance(zd, mnmajor_step_bytes(ks)),
+                   desc_advance(pd, mnmajor_step_bytes(ks)), id_o2, ks > 0);
+        }
+        mma_commit(&bb.o_done);
+      } else {
+        ok = mbar_wait(&bb.z_full, ph, err, abort_flag);
+        tc_fence_after();
+      }
+      if (ok) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          const uint64_t yd = desc_mnmajor_base(smem_u32(smem + L::kYs + q * L::kT), 64);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ss(tmem, desc_advance(zd, mnmajor_step_bytes(ks)),
+                   desc_advance(yd, mnmajor_step_bytes(ks)), id_u, 1);
+        }
+      }
+      mma_commit(&bb.u_done);
+    }
+    __syncwarp();
+    if (!kStateOnly) {
+      ok = mbar_wait(&bb.o_done, ph, err, abort_flag) && ok;
+      tc_fence_after();
+      if (t == 0 && ok && c + 1 < chunks) load(tm_x, L::kX, &bb.x_full, c + 1);
+      __syncwarp();
+      if (ok && (warp & 3) * 32 < D) {
+        float o1[32], o2[32];
+        tmem_ld32(tO1 + wg * 32, o1);
+        tmem_ld32(tA + wg * 32, o2);
+        tmem_ld_wait();
+        __nv_bfloat16* dst =
+            g.r.out.p + (size_t(pc.row) + row0 + wg * 32) * g.r.out.row + h * g.r.out.head + z;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int k = wg * 32 + e;
+          if (k < r)
+            dst[e * g.r.out.row] =
+                __float2bfloat16(fmaf(o1[e], g.f_inter * pw[rev ? r - 1 - k : k + 1], o2[e]));
+        }
+      }
+    }
+    ok = mbar_wait(&bb.u_done, ph, err, abort_flag) && ok;
+    tc_fence_after();
+    if (t == 0 && ok && c + 1 < chunks) load(tm_z, L::kZ, &bb.z_full, c + 1);
+    tc_fence_before();
+    ok = __syncthreads_and(ok);
+    tc_fence_after();
+    if (!ok) break;
+  }
+
+  if (!ok) {
+    // let copies and products already in flight end before the CTA exits (a barrier
+    // without one runs into its time limit)
+    if (t == 0) {
+      for (uint32_t q = 0; q < 2; ++q) {
+        mbar_wait(&bb.x_full, q, nullptr, nullptr);
+        mbar_wait(&bb.y_full, q, nullptr, nullptr);
+        mbar_wait(&bb.z_full, q, nullptr, nullptr);
+        mbar_wait(&bb.u_done, q, nullptr, nullptr);
+      }
+    }
+  } else if (kStateOnly || (g.r.state_out && (rev ? pc.first : pc.last))) {
+    float* dst = kStateOnly ? g.states + (size_t(pc.slot) * g.H + h) * D * D
+                            : g.r.state_out + (size_t(pc.seq) * g.H + h) * D * D;
+#pragma unroll 1
+    for (int c0 = 0; c0 < kHalf; c0 += 16) {
+      float v[16];
+      tmem_ld16(tS + c0, v);
+      tmem_ld_wait();
+      if (z < D) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) dst[size_t(wg * kHalf + c0 + e) * D + z] = v[e];
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_free(tmem, 256);
+}
+
+// The states before the pieces of the cut sequences, over their sums: with U_j
+// the j-th piece's sum and n_j its rows,  S_0 = state_in,  S_{j+1} = l^{n_j} S_j + U_j.
+// Four elements per thread.
+template <int D>
+__global__ void __launch_bounds__(256) decay_scan_kernel(const int* __restrict__ counts,
+                                                         const Split* __restrict__ splits,
+                                                         float* __restrict__ states,
+                                                         const float* __restrict__ log_decay,
+                                                         DecayRun r, int H, int rows) {
+  if (int(blockIdx.x) >= counts[1]) return;
+  const Split sp = splits[blockIdx.x];
+  const int h = blockIdx.y, e = (blockIdx.z * 256 + threadIdx.x) * 4;
+  const float gl = decay_checked(log_decay[h]);
+  const Factor full = decay_factor(gl, rows), part = decay_factor(gl, sp.last_rows);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r.state_in) {
+    const float* p = r.state_in + (size_t(sp.seq) * H + h) * D * D;
+    const int y = e / D, z = e % D;
+    s = r.state_t ? make_float4(p[z * D + y], p[(z + 1) * D + y], p[(z + 2) * D + y],
+                                p[(z + 3) * D + y])
+                  : *reinterpret_cast<const float4*>(p + e);
+  }
+  for (int j = 0; j < sp.pieces; ++j) {
+    const int k = r.reverse ? sp.pieces - 1 - j : j;
+    float4* at = reinterpret_cast<float4*>(states + (size_t(sp.slot + k) * H + h) * D * D + e);
+    const bool last = j == sp.pieces - 1;
+    const float4 u = last ? s : *at;
+    *at = s;
+    const Factor f = k == sp.pieces - 1 ? part : full;
+    s = make_float4(scaled(s.x, f) + u.x, scaled(s.y, f) + u.y, scaled(s.z, f) + u.z,
+                    scaled(s.w, f) + u.w);
   }
 }
 
@@ -102,15 +439,54 @@ __global__ void __launch_bounds__(256) decay_step_kernel(
 
 }  // namespace
 
-cudaError_t launch_decay_run(const DecayProblem& p, const DecayRun& r, const Seq* seqs,
-                             const float* log_decay, int* err, cudaStream_t s) {
-  (void)err;
-  const dim3 grid(p.n_seq, p.H);
-  const float fo = r.reverse ? 1.f : p.scale, fu = r.reverse ? p.scale : 1.f;
+namespace {
+
+template <int D, bool kStateOnly>
+cudaError_t run(const DecayProblem& p, const DecayCut& cut, const DecayRun& r, const DecayLists& l,
+                const float* log_decay, int* err, cudaStream_t s) {
+  const auto map = [&](CUtensorMap* m, const RowView& v) {
+    return make_tmap_rows(m, v.p, p.total, p.H, D, sla_strides{v.row, v.head}, 64);
+  };
+  CUtensorMap tx, ty, tz;
+  if (!map(&tx, r.x) || !map(&ty, r.y) || !map(&tz, r.z)) return cudaErrorInvalidValue;
+  const DrArgs a{l.counts,       l.pieces, l.states,
+                 log_decay,      r,        p.H,
+                 cut.most_slots, p.scale,  r.reverse ? 1.f : p.scale,
+                 r.reverse ? p.scale : 1.f, err};
+  auto* kernel = decay_run_kernel<D, kStateOnly>;
+  const cudaError_t e = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DrSmem<D>::kTotal);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = unsigned(cut.most_slots + (kStateOnly ? 0 : p.n_seq)) * p.H;
+  kernel<<<grid, 256, DrSmem<D>::kTotal, s>>>(tx, ty, tz, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decay_run(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+                             const DecayLists& l, const float* log_decay, int* err,
+                             cudaStream_t s) {
+  return p.d == 128 ? run<128, false>(p, cut, r, l, log_decay, err, s)
+                    : run<64, false>(p, cut, r, l, log_decay, err, s);
+}
+
+cudaError_t launch_decay_pieces(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+                                const DecayLists& l, const float* log_decay, int* err,
+                                cudaStream_t s) {
+  return p.d == 128 ? run<128, true>(p, cut, r, l, log_decay, err, s)
+                    : run<64, true>(p, cut, r, l, log_decay, err, s);
+}
+
+cudaError_t launch_decay_scan(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+                              const DecayLists& l, const float* log_decay, cudaStream_t s) {
+  const dim3 grid(cut.most_splits, p.H, p.d * p.d / 1024);
   if (p.d == 128)
-    decay_run_kernel<128><<<grid, 128, 0, s>>>(r, seqs, log_decay, p.H, fo, fu);
+    decay_scan_kernel<128><<<grid, 256, 0, s>>>(l.counts, l.splits, l.states, log_decay, r, p.H,
+                                                cut.rows);
   else
-    decay_run_kernel<64><<<grid, 64, 0, s>>>(r, seqs, log_decay, p.H, fo, fu);
+    decay_scan_kernel<64><<<grid, 256, 0, s>>>(l.counts, l.splits, l.states, log_decay, r, p.H,
+                                               cut.rows);
   return cudaGetLastError();
 }
 

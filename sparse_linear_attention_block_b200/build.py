@@ -26,7 +26,7 @@ LIB = os.path.join(PKG_DIR, "libsla.so")
 SOURCES = ["sla_api.cu", "sla_classify.cu", "sla_linear.cu", "sla_fwd_linear.cu",
            "sla_sparse_fwd.cu", "sla_bwd_linear.cu", "sla_sparse_bwd.cu", "sla_noalloc.cu",
            "sla_causal_api.cu", "sla_causal_plan.cu", "sla_causal_fwd.cu", "sla_causal_bwd.cu",
-           "sla_decay.cu"]
+           "sla_causal_token.cu", "sla_decay.cu"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMPILE_FLAGS = ARCH + [

@@ -27,6 +27,12 @@ struct Seq {
   int q0, nq, k0, nk;
 };
 
+// The caller's offsets.
+struct SeqIn {
+  const int32_t *q_off, *k_off, *k_len;
+  int n_seq, total_q, total_k, max_q;
+};
+
 // One tile of a causal kernel's work list: tile number `tile` of sequence `seq`.
 struct alignas(16) Item {
   Seq s;
@@ -113,11 +119,14 @@ struct CausalPlan {
   Item* k_items;  // may be null
   int* k_count;
 };
-cudaError_t launch_causal_plan(const CausalProblem& p, const int32_t* q_off, const int32_t* k_off,
-                               const int32_t* k_len, const CausalPlan& plan, int* err,
-                               cudaStream_t s);
+cudaError_t launch_causal_plan(const SeqIn& in, const CausalPlan& plan, int* err, cudaStream_t s);
 cudaError_t launch_causal_fwd(const CausalProblem& p, const void* q, const void* k, const void* v,
                               const ItemList& list, void* o, float* lse, int* err, cudaStream_t s);
+// A few queries per sequence: max_q G rows at most kTokenRows.
+constexpr int kTokenRows = 64;
+cudaError_t launch_causal_token(const CausalProblem& p, const void* q, const void* k,
+                                const void* v, const SeqIn& in, void* o, float* lse, int* err,
+                                cudaStream_t s);
 cudaError_t launch_causal_dvec(const CausalProblem& p, const void* o, const void* d_o, float* dvec,
                                cudaStream_t s);
 cudaError_t launch_causal_dq(const CausalProblem& p, const void* q, const void* k, const void* v,
@@ -182,6 +191,15 @@ __device__ __forceinline__ Factor decay_factor(float g, int n) {
 }
 __device__ __forceinline__ float scaled(float s, const Factor& f) { return fmaf(s, f.hi, s * f.lo); }
 __device__ __forceinline__ float decay_checked(float g) { return g <= 0.f ? g : 0.f; }
+
+// Sequence i, empty and *good = false if its offsets decrease, leave the tensor or exceed max_q.
+__device__ __forceinline__ Seq checked_seq(const SeqIn& in, int i, bool* good) {
+  const long long q0 = in.q_off[i], q1 = in.q_off[i + 1], k0 = in.k_off[i];
+  const long long k1 = in.k_len ? k0 + in.k_len[i] : in.k_off[i + 1];
+  *good = q0 >= 0 && q1 >= q0 && q1 <= in.total_q && q1 - q0 <= in.max_q && k0 >= 0 && k1 >= k0 &&
+          k1 <= in.total_k;
+  return *good ? Seq{int(q0), int(q1 - q0), int(k0), int(k1 - k0)} : Seq{0, 0, 0, 0};
+}
 
 // Write 8 consecutive 32-bit TMEM columns of a warp's 32 lanes.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {

@@ -62,7 +62,8 @@ sla_status check_causal(const sla_causal_shape* s, CausalProblem* p) {
   // grids: one CTA for each tile and head
   const size_t tiles = most_items(s->total_q > s->total_k ? s->total_q : s->total_k, kRowTile,
                                   s->n_seq);
-  if (tiles * size_t(s->Hq) >= (1u << 31)) return SLA_ERR_UNSUPPORTED;
+  if (tiles * size_t(s->Hq) >= (1u << 31) || size_t(s->n_seq) * s->Hq >= (1u << 29))
+    return SLA_ERR_UNSUPPORTED;
   return SLA_OK;
 }
 
@@ -203,11 +204,19 @@ sla_status sla_causal_forward(const sla_causal_shape* shape, const void* q, cons
   if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = at<int>(workspace, L.err);
+  const SeqIn in{q_off, k_off, k_len, p.n_seq, p.total_q, p.total_k, p.max_q};
+  // generated tokens: the 128-query tiles would be almost empty, and there would be too few of
+  // them (48 caches of up to 8192 keys, 16 heads over 4: 212 us with them, 81 us this way;
+  // one cache of 4001 keys, 12 heads over 4: 65 us and 8.8 us)
+  if ((long long)p.max_q * p.G <= kTokenRows) {
+    SLA_LAUNCH("causal_token", s, launch_causal_token(p, q, k, v, in, o, lse, err, s));
+    return SLA_OK;
+  }
   int* counts = at<int>(workspace, L.counts);
   Item* items = at<Item>(workspace, L.items);
   const int most = int(most_items(p.total_q, fwd_tile(p), p.n_seq));
   const CausalPlan plan{fwd_tile(p), most, items, counts, 0, nullptr, nullptr};
-  SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, k_len, plan, err, s));
+  SLA_LAUNCH("causal_plan", s, launch_causal_plan(in, plan, err, s));
   const ItemList list{counts, items, most};
   SLA_LAUNCH("causal_fwd", s, launch_causal_fwd(p, q, k, v, list, o, lse, err, s));
   return SLA_OK;
@@ -228,13 +237,14 @@ sla_status sla_causal_backward(const sla_causal_shape* shape, const void* q, con
   if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = at<int>(workspace, L.err);
+  const SeqIn in{q_off, k_off, nullptr, p.n_seq, p.total_q, p.total_k, p.max_q};
   int* counts = at<int>(workspace, L.counts);
   Item *items = at<Item>(workspace, L.items), *kitems = at<Item>(workspace, L.kitems);
   float* dvec = at<float>(workspace, L.dvec);
   const int most = int(most_items(p.total_q, fwd_tile(p), p.n_seq)),
             kmost = int(most_items(p.total_k, kRowTile, p.n_seq));
   const CausalPlan plan{fwd_tile(p), most, items, counts, kmost, kitems, counts + 1};
-  SLA_LAUNCH("causal_plan", s, launch_causal_plan(p, q_off, k_off, nullptr, plan, err, s));
+  SLA_LAUNCH("causal_plan", s, launch_causal_plan(in, plan, err, s));
   const ItemList list{counts, items, most};
   const ItemList klist{counts + 1, kitems, kmost};
   SLA_LAUNCH("causal_dvec", s, launch_causal_dvec(p, o, d_o, dvec, s));

@@ -8,22 +8,6 @@ namespace {
 
 constexpr int kPlanThreads = 1024, kBuckets = 2048;
 
-struct PlanIn {
-  const int32_t *q_off, *k_off, *k_len;
-  int n_seq, total_q, total_k, max_q, shift;
-};
-
-// A sequence whose offsets decrease, leave the tensor or exceed max_q is
-// replaced by an empty one and reported.
-__device__ __forceinline__ Seq checked_seq(const PlanIn& in, int i, int* err) {
-  const long long q0 = in.q_off[i], q1 = in.q_off[i + 1], k0 = in.k_off[i];
-  const long long k1 = in.k_len ? k0 + in.k_len[i] : in.k_off[i + 1];
-  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= in.total_q && q1 - q0 <= in.max_q && k0 >= 0 &&
-                  k1 >= k0 && k1 <= in.total_k;
-  if (!ok && lane_id() == 0) set_error(err, SLA_ERR_DEVICE);
-  return ok ? Seq{int(q0), int(q1 - q0), int(k0), int(k1 - k0)} : Seq{0, 0, 0, 0};
-}
-
 // Keys that query tile t sees, or queries that see key tile t, in 128s.
 __device__ __forceinline__ int item_cost(const Seq& s, int t, int tile, bool keys) {
   const long long off = (long long)s.nk - s.nq;
@@ -41,8 +25,8 @@ __device__ __forceinline__ int item_cost(const Seq& s, int t, int tile, bool key
 // it.  A warp takes a sequence, a lane a tile; one sequence of 16384 rows and
 // sixteen short ones take about 4 us either way, bound by the latency of the
 // chain offsets -> histogram -> scan -> scatter.
-__global__ void __launch_bounds__(kPlanThreads) causal_plan_kernel(PlanIn in, CausalPlan plan,
-                                                                   int* err) {
+__global__ void __launch_bounds__(kPlanThreads) causal_plan_kernel(SeqIn in, int shift,
+                                                                   CausalPlan plan, int* err) {
   __shared__ int hist[kBuckets], warp_sum[32];
   const bool keys = blockIdx.x == 1;
   const int tile = keys ? kRowTile : plan.q_tile;
@@ -51,9 +35,11 @@ __global__ void __launch_bounds__(kPlanThreads) causal_plan_kernel(PlanIn in, Ca
   const int t = threadIdx.x, warp = t / 32, lane = t % 32;
   for (int b = t; b < kBuckets; b += kPlanThreads) hist[b] = 0;
   __syncthreads();
-  auto bucket = [&](int cost) { return kBuckets - 1 - min(cost >> in.shift, kBuckets - 1); };
+  auto bucket = [&](int cost) { return kBuckets - 1 - min(cost >> shift, kBuckets - 1); };
   for (int i = warp; i < in.n_seq; i += kPlanThreads / 32) {
-    const Seq s = checked_seq(in, i, err);
+    bool good;
+    const Seq s = checked_seq(in, i, &good);
+    if (!good && lane == 0) set_error(err, SLA_ERR_DEVICE);
     const int n = ((keys ? s.nk : s.nq) + tile - 1) / tile;
     for (int j = lane; j < n; j += 32) atomicAdd(&hist[bucket(item_cost(s, j, tile, keys))], 1);
   }
@@ -89,7 +75,8 @@ __global__ void __launch_bounds__(kPlanThreads) causal_plan_kernel(PlanIn in, Ca
   hist[2 * t + 1] = before + a;
   __syncthreads();
   for (int i = warp; i < in.n_seq; i += kPlanThreads / 32) {
-    const Seq s = checked_seq(in, i, err);
+    bool good;
+    const Seq s = checked_seq(in, i, &good);
     const int n = ((keys ? s.nk : s.nq) + tile - 1) / tile;
     for (int j = lane; j < n; j += 32) {
       const int at = atomicAdd(&hist[bucket(item_cost(s, j, tile, keys))], 1);
@@ -152,14 +139,11 @@ __global__ void __launch_bounds__(kPlanThreads) decay_plan_kernel(
 
 }  // namespace
 
-cudaError_t launch_causal_plan(const CausalProblem& p, const int32_t* q_off, const int32_t* k_off,
-                               const int32_t* k_len, const CausalPlan& plan, int* err,
-                               cudaStream_t s) {
-  const int most = (p.total_k > p.total_q ? p.total_k : p.total_q) / 128 + 2;
+cudaError_t launch_causal_plan(const SeqIn& in, const CausalPlan& plan, int* err, cudaStream_t s) {
+  const int most = (in.total_k > in.total_q ? in.total_k : in.total_q) / 128 + 2;
   int shift = 0;
   while ((most >> shift) >= kBuckets) ++shift;
-  const PlanIn in{q_off, k_off, k_len, p.n_seq, p.total_q, p.total_k, p.max_q, shift};
-  causal_plan_kernel<<<plan.k_items ? 2 : 1, kPlanThreads, 0, s>>>(in, plan, err);
+  causal_plan_kernel<<<plan.k_items ? 2 : 1, kPlanThreads, 0, s>>>(in, shift, plan, err);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,375 @@
+// Causal softmax attention of a few queries per sequence against many keys
+// (generated tokens), forward: the same formulas as sla_causal_fwd.cu.
+//
+// A sequence's queries of the heads that share a key head are rows of one
+// matrix, row a G + g, in tiles of 16, so that a group reads its keys once.
+// Bound by the bytes of K and V: the products (mma.sync, M = 16) need about a
+// third of the time that the bytes take.  With so few rows tcgen05 (M = 128)
+// would spend its instructions on empty ones and could not split the keys of a
+// tile over warps.
+//
+// A cluster of CTAs splits a sequence's keys into equal runs of 64-key tiles; in
+// a CTA a TMA thread fills a ring of three K/V tiles and each of four warps
+// takes 16 keys of every tile, with a running maximum and sum of its own
+// (fp32).  The partial results are joined over the warps in shared memory, then
+// over the cluster in distributed shared memory, always in the same order.  One
+// launch, no workspace but the error word.
+#include <cooperative_groups.h>
+
+#include "sla_causal.h"
+#include "sla_ptx.cuh"
+
+namespace sla {
+namespace {
+
+constexpr int kWarps = 4, kThreads = (kWarps + 1) * 32, kSt = 3, kRows = 16;
+
+template <int D>
+struct CtSmem {
+  static constexpr int kT = 64 * D * 2;             // 64 keys of K or V
+  static constexpr int kTiles = kSt * 2 * kT;       // the ring, then the warps' partial sums
+  static constexpr int kPitch = D + 4;              // floats per row of a partial sum
+  static constexpr int kO = kTiles;                 // fp32 [16][D]: the CTA's sum
+  static constexpr int kMl = kO + kRows * D * 4;    // m[16], l[16]
+  static constexpr int kWml = kMl + 2 * kRows * 4;  // the warps' m, l
+  static constexpr int kBars = kWml + kWarps * 2 * kRows * 4;
+  static constexpr int kTotal = kBars + 2 * kSt * 8 + 16;
+  static_assert(kWarps * kRows * kPitch * 4 <= kTiles, "partial sums fit the ring");
+};
+
+struct CtArgs {
+  SeqIn in;
+  const __nv_bfloat16* q;
+  long long q_row, q_head;
+  __nv_bfloat16* o;
+  long long o_row, o_head;
+  float* lse;
+  int Hkv, G, row_tiles, splits;
+  float scale_log2;
+  int* err;
+};
+
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// exp2 of a difference of running maxima, 0 for a part that has seen nothing
+__device__ __forceinline__ float weight(float m, float top) {
+  return m == -INFINITY ? 0.f : exp2f(m - top);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) causal_token_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const CtArgs g) {
+  using L = CtSmem<D>;
+  namespace cg = cooperative_groups;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int split = blockIdx.x % g.splits;
+  int u = blockIdx.x / g.splits;
+  const int hk = u % g.Hkv;
+  u /= g.Hkv;
+  const int rt = u % g.row_tiles, i = u / g.row_tiles;
+  bool ok = (smem_u32(smem) & 1023u) == 0u;  // no static shared memory: the window's start
+  if (!ok && threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
+  bool good;
+  Seq s = checked_seq(g.in, i, &good);
+  if (!good && threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
+  if (!ok || rt * kRows >= s.nq * g.G) return;  // the whole cluster
+
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* empty = full + kSt;
+  int* abort_word = reinterpret_cast<int*>(empty + kSt);
+  volatile int* abort_flag = abort_word;
+  float* sO = reinterpret_cast<float*>(smem + L::kO);
+  float* sMl = reinterpret_cast<float*>(smem + L::kMl);
+  float* sWml = reinterpret_cast<float*>(smem + L::kWml);
+  const int t = threadIdx.x, warp = t / 32, lane = t % 32;
+  if (t == 0) {
+    for (int k = 0; k < kSt; ++k) {
+      mbar_init(&full[k], 1);
+      mbar_init(&empty[k], kWarps);
+    }
+    *abort_word = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+
+  // this CTA's tiles: the keys that the tile's last row sees
+  const int a_last = min(s.nq - 1, (rt * kRows + kRows - 1) / g.G);
+  const int keys = max(0, min(s.nk, s.nk - s.nq + a_last + 1));
+  const int tiles = (keys + 63) / 64;
+  const int t0 = int((long long)tiles * split / g.splits),
+            t1 = int((long long)tiles * (split + 1) / g.splits);
+
+  if (warp == kWarps) {
+    if (lane == 0) {
+      int k = t0;
+      for (; k < t1; ++k) {
+        const int n = k - t0, st = n % kSt;
+        if (n >= kSt && !mbar_wait(&empty[st], ((n / kSt) + 1) & 1, g.err, abort_flag)) break;
+        mbar_arrive_expect_tx(&full[st], 2 * L::kT);
+        uint8_t* dst = smem + st * 2 * L::kT;
+        for (int c = 0; c < D / 64; ++c) {
+          tma_load_3d(dst + c * 8192, &full[st], &tm_k, c * 64, s.k0 + k * 64, hk);
+          tma_load_3d(dst + L::kT + c * 8192, &full[st], &tm_v, c * 64, s.k0 + k * 64, hk);
+        }
+      }
+      // every copy has landed before the ring's memory is used for the sums
+      for (int n = max(0, k - t0 - kSt); n < k - t0; ++n)
+        mbar_wait(&full[n % kSt], (n / kSt) & 1, g.err, nullptr);
+    }
+  } else {
+    // Q fragments of the 16 rows: lane l holds rows l / 4 and l / 4 + 8
+    uint32_t qf[D / 16][4];
+    int lim[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = rt * kRows + lane / 4 + x * 8, a = r / g.G;
+      const bool real = a < s.nq;
+      lim[x] = real ? min(s.nk, s.nk - s.nq + a + 1) : 0;
+      const __nv_bfloat16* p =
+          g.q + (size_t(s.q0) + (real ? a : 0)) * g.q_row + (hk * g.G + r % g.G) * g.q_head;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(p + ks * 16 + (lane % 4) * 2);
+        qf[ks][x] = real ? w[0] : 0u;
+        qf[ks][x + 2] = real ? w[4] : 0u;
+      }
+    }
+    float acc[D / 8][4];
+#pragma unroll
+    for (int e = 0; e < D / 8; ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    const int key0 = warp * 16;
+    // ldmatrix rows of this lane: K by keys (lane % 8, + 8 for the upper matrices) and
+    // 8-feature halves, V by keys and 8-feature columns
+    const int kr = key0 + (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+    const int vr = key0 + (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
+    for (int k = t0; k < t1; ++k) {
+      const int n = k - t0, st = n % kSt;
+      if (!mbar_wait(&full[st], (n / kSt) & 1, g.err, abort_flag)) break;
+      uint8_t* tk = smem + st * 2 * L::kT;
+      uint8_t* tv = tk + L::kT;
+      const int left = s.nk - k * 64 - key0;  // keys of the sequence from this warp's first on
+      if (left < 16) {  // clear the rows of V behind them: 0 times NaN would be NaN
+        for (int e = max(0, left) * 8 + lane; e < 128; e += 32)
+          for (int c = 0; c < D / 64; ++c)
+            *reinterpret_cast<uint4*>(tv + c * 8192 + (key0 + e / 8) * 128 + (e % 8) * 16) =
+                make_uint4(0, 0, 0, 0);
+        __syncwarp();
+      }
+      float sc[2][4] = {};
+      const uint32_t kb = smem_u32(tk), vb = smem_u32(tv);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t b[4];
+        const int unit = (ks & 3) * 2 + kc;
+        ldm4(b, kb + (ks >> 2) * 8192 + kr * 128 + ((unit ^ (kr & 7)) << 4));
+        mma16816(sc[0], qf[ks], b[0], b[1]);
+        mma16816(sc[1], qf[ks], b[2], b[3]);
+      }
+      const int b0 = k * 64 + key0 + (lane % 4) * 2;
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = b0 + j * 8 + (e & 1);
+          sc[j][e] = key < lim[e >> 1] ? sc[j][e] * g.scale_log2 : -INFINITY;
+          top[e >> 1] = fmaxf(top[e >> 1], sc[j][e]);
+        }
+      float f[2], base[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+        top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+        const float mn = fmaxf(m[x], top[x]);
+        f[x] = weight(m[x], mn);
+        m[x] = mn;
+        base[x] = mn == -INFINITY ? 0.f : mn;
+        l[x] *= f[x];
+      }
+      uint32_t pf[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float p0 = exp2f(sc[j][2 * x] - base[x]), p1 = exp2f(sc[j][2 * x + 1] - base[x]);
+          l[x] += p0 + p1;
+          pf[j * 2 + x] = pack_bf16(p0, p1);
+        }
+      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+          acc[e][0] *= f[0];
+          acc[e][1] *= f[0];
+          acc[e][2] *= f[1];
+          acc[e][3] *= f[1];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) {
+        uint32_t b[4];
+        const int unit = (e & 3) * 2 + vc;
+        ldm4t(b, vb + (e >> 2) * 8192 + vr * 128 + ((unit ^ (vr & 7)) << 4));
+        mma16816(acc[2 * e], pf, b[0], b[1]);
+        mma16816(acc[2 * e + 1], pf, b[2], b[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    }
+    // all four warps are through with the ring before their sums go there
+    named_bar_sync(1, kWarps * 32);
+    float* part = reinterpret_cast<float*>(smem) + warp * kRows * L::kPitch;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = lane / 4 + x * 8;
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e)
+        *reinterpret_cast<float2*>(part + r * L::kPitch + e * 8 + (lane % 4) * 2) =
+            make_float2(acc[e][2 * x], acc[e][2 * x + 1]);
+      if (lane % 4 == 0) {
+        sWml[warp * 2 * kRows + r] = m[x];
+        sWml[warp * 2 * kRows + kRows + r] = l[x];
+      }
+    }
+  }
+  __syncthreads();
+  // join the warps
+  for (int e = t; e < kRows * D / 4; e += kThreads) {
+    const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sWml[w * 2 * kRows + r]);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = weight(sWml[w * 2 * kRows + r], top);
+      const float4 p = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
+                                                        (w * kRows + r) * L::kPitch + c);
+      l += f * sWml[w * 2 * kRows + kRows + r];
+      sum.x += f * p.x;
+      sum.y += f * p.y;
+      sum.z += f * p.z;
+      sum.w += f * p.w;
+    }
+    *reinterpret_cast<float4*>(sO + r * D + c) = sum;
+    if (c == 0) {
+      sMl[r] = top;
+      sMl[kRows + r] = l;
+    }
+  }
+  // join the cluster: every CTA writes its share of the rows' pieces of 8 features
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (int e = split + g.splits * t; e < kRows * D / 8; e += g.splits * kThreads) {
+    const int r = e / (D / 8), c = (e % (D / 8)) * 8, row = rt * kRows + r, a = row / g.G;
+    if (a >= s.nq) continue;
+    float top = -INFINITY;
+    for (int k = 0; k < g.splits; ++k) top = fmaxf(top, cluster.map_shared_rank(sMl, k)[r]);
+    float sum[8] = {}, l = 0.f;
+    for (int k = 0; k < g.splits; ++k) {
+      const float* ml = cluster.map_shared_rank(sMl, k);
+      const float f = weight(ml[r], top);
+      l += f * ml[kRows + r];
+      const float4* p = reinterpret_cast<const float4*>(cluster.map_shared_rank(sO, k) + r * D + c);
+      const float4 x = p[0], y = p[1];
+      sum[0] += f * x.x;
+      sum[1] += f * x.y;
+      sum[2] += f * x.z;
+      sum[3] += f * x.w;
+      sum[4] += f * y.x;
+      sum[5] += f * y.y;
+      sum[6] += f * y.z;
+      sum[7] += f * y.w;
+    }
+    const bool some = l > 0.f;
+    const float inv = some ? 1.f / l : 0.f;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = some ? pack_bf16(sum[2 * k] * inv, sum[2 * k + 1] * inv) : 0u;
+    const int head = hk * g.G + row % g.G;
+    *reinterpret_cast<uint4*>(g.o + (size_t(s.q0) + a) * g.o_row + head * g.o_head + c) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+    if (c == 0)
+      g.lse[size_t(head) * g.in.total_q + s.q0 + a] =
+          some ? (top + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
+  }
+  cluster.sync();  // nobody leaves while its shared memory is read
+}
+
+template <int D>
+cudaError_t launch(const CtArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, unsigned units,
+                   cudaStream_t s) {
+  auto* kernel = causal_token_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       CtSmem<D>::kTotal);
+  if (e == cudaSuccess && a.splits > 8)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(a.splits);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(units * unsigned(a.splits));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = CtSmem<D>::kTotal;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_causal_token(const CausalProblem& p, const void* q, const void* k,
+                                const void* v, const SeqIn& in, void* o, float* lse, int* err,
+                                cudaStream_t s) {
+  CUtensorMap tk, tv;
+  if (!make_tmap_rows(&tk, k, p.total_k, p.Hkv, p.d, p.k, 64) ||
+      !make_tmap_rows(&tv, v, p.total_k, p.Hkv, p.d, p.v, 64))
+    return cudaErrorInvalidValue;
+  const int row_tiles = (p.max_q * p.G + kRows - 1) / kRows;
+  const unsigned units = unsigned(p.n_seq) * p.Hkv * row_tiles;
+  // two CTAs fit on an SM: split the keys while there are fewer CTAs than that, and while a
+  // split keeps four tiles of the longest possible sequence
+  int splits = 1;
+  while (splits < 16 && units * splits < 2 * 148 && splits * 2 * 256 <= p.total_k) splits *= 2;
+  const CtArgs a{in,      static_cast<const __nv_bfloat16*>(q),
+                 p.q.row, p.q.head,
+                 static_cast<__nv_bfloat16*>(o),
+                 p.o.row, p.o.head,
+                 lse,     p.Hkv,
+                 p.G,     row_tiles,
+                 splits,  p.scale_log2,
+                 err};
+  return p.d == 128 ? launch<128>(a, tk, tv, units, s) : launch<64>(a, tk, tv, units, s);
+}
+
+}  // namespace sla

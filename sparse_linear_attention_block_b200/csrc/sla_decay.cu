@@ -15,25 +15,26 @@ namespace sla {
 namespace {
 
 // Design of a run (sm_100a).  A CTA (256 threads, two CTAs per SM) walks a piece
-// of a sequence in chunks of 64 tokens with the state as S^T [z][y] in TMEM
+// of a sequence in chunks of 64 tokens with the state S^T [z][y] in registers
 // (fp32).  Per chunk of r tokens, w_n = l^n, forward (reversed runs mirror the
 // exponents):
 //   A[s][t]  = y_s . x_t                          MMA, tokens s on the lanes
-//   P[s][t]  = w_{t-s} A[s][t]  (s <= t)          bf16, to shared memory
 //   O1[z][t] = sum_y S[z][y] x_t[y]               MMA, S rounded to bf16 in TMEM
+//   P[s][t]  = w_{t-s} A[s][t]  (s <= t)          bf16, to shared memory
 //   O2[z][t] = sum_s z_s P[s][t]                  MMA
-//   out_t    = w_{t+1} O1[.][t] + O2[.][t]
-//   S        = w_r S + sum_s z_s (w_{r-1-s} y_s)^T   MMA on top of w_r S
+//   U[z][y]  = sum_s z_s w_{r-1-s} y_s            MMA
+//   out_t    = w_{t+1} O1[.][t] + O2[.][t],  S = w_r S + U
 // The state is held to 32 bits: w y is fed as three bf16 numbers (their sum has
-// 24 bits) and w_r S is a product with a two-number factor; only what a query
+// 24 bits), U starts from 0 in every chunk (the tensor core's sums truncate, a
+// running one would drift) and w_r is a two-number factor; only what a query
 // reads (S and P as operands) is rounded to bf16, like the output.
 // The features lie on the TMEM lanes everywhere (M = 128, for d = 64 with lanes
-// that nobody reads), so the state goes from its accumulator to an A operand
-// without leaving its lanes.  TMEM: S at 0, A then S (bf16) then O2 at 128, O1
-// at 192: 256 columns.
+// that nobody reads), so the state goes into an A operand without leaving its
+// lanes.  TMEM: S (bf16), then U at 0, A, then O2 at 128, O1 at 192: 256 columns.
 // The bytes of a chunk (x, y, z, out) take longer than its products; what is
 // to be hidden is the chain state -> S in bf16 -> products -> state, which two
-// CTAs per SM do for one another.
+// CTAs per SM do for one another.  A and O1 run while w y is split, the output
+// is written while U runs.
 template <int D>
 struct DrSmem {
   static constexpr int kT = 64 * D * 2;                      // x, y or z of a chunk
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
   tc_fence_after();
   const uint32_t tmem = bb.tmem_base;
   const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
-  const uint32_t tS = tmem + lane_base + wg * kHalf, tA = tmem + lane_base + 128,
+  const uint32_t tU = tmem + lane_base + wg * kHalf, tA = tmem + lane_base + 128,
                  tO1 = tmem + lane_base + 192;
   const int chunks = (pc.rows + 63) / 64;
   // rows of the c-th chunk in walking order
@@ -123,7 +124,8 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
     load(tm_z, L::kZ, &bb.z_full, 0);
   }
 
-  // the state before the piece
+  // the state before the piece: a thread keeps kHalf columns of its lane's row
+  float S[kHalf];
   {
     const size_t dd = size_t(D) * D;
     const float* src = nullptr;
@@ -136,36 +138,59 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
         turned = g.r.state_t;
       }
     }
-#pragma unroll 1
-    for (int c0 = 0; c0 < kHalf; c0 += 16) {
+#pragma unroll
+    for (int e = 0; e < kHalf; ++e) {
+      const int y = wg * kHalf + e;
+      S[e] = src && z < D ? src[turned ? z * D + y : y * D + z] : 0.f;
+    }
+  }
+  // what a query reads: the state rounded to bf16, as an operand over the place of U
+  auto put_state = [&]() {
+#pragma unroll
+    for (int q = 0; q < kHalf / 2; q += 16) {
       uint32_t w[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int y = wg * kHalf + c0 + e;
-        w[e] = src && z < D ? __float_as_uint(src[turned ? z * D + y : y * D + z]) : 0u;
-      }
-      tmem_st16(tS + c0, w);
+      for (int e = 0; e < 16; ++e) w[e] = pack_bf16(S[2 * (q + e)], S[2 * (q + e) + 1]);
+      tmem_st16(tU + q, w);
     }
     tmem_st_wait();
-  }
+  };
+  // A = Y X^T and O1 = S X^T of chunk c (one thread)
+  auto issue_ao = [&](int c) -> bool {
+    constexpr uint32_t id_a = idesc_bf16(128, 64, 0, 0);
+    if (!mbar_wait(&bb.y_full, c & 1, err, abort_flag) ||
+        !mbar_wait(&bb.x_full, c & 1, err, abort_flag))
+      return false;
+    tc_fence_after();
+    const uint64_t yd = desc_kmajor_base(smem_u32(smem + L::kY)),
+                   xd = desc_kmajor_base(smem_u32(smem + L::kX));
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+      mma_ss(tmem + 128, desc_advance(yd, kmajor_step_bytes(64, ks)),
+             desc_advance(xd, kmajor_step_bytes(64, ks)), id_a, ks > 0);
+    constexpr int kPer = D / 32;  // k-steps of a warpgroup's half of the state
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+      mma_ts(tmem + 192, tmem + (ks / kPer) * kHalf + (ks % kPer) * 8,
+             desc_advance(xd, kmajor_step_bytes(64, ks)), id_a, ks > 0);
+    mma_commit(&bb.a_done);
+    return true;
+  };
   const Factor whole = decay_factor(gl, 64);
   bool ok = true;
+  if (!kStateOnly && chunks > 0) {
+    put_state();
+    tc_fence_before();
+    __syncthreads();
+    if (t == 0) ok = issue_ao(0);
+    __syncwarp();
+  }
 
   for (int c = 0; c < chunks; ++c) {
     const int row0 = chunk_row(c), r = min(64, pc.rows - row0);
     const uint32_t ph = c & 1;
-    const Factor carry = r < 64 ? decay_factor(gl, r) : whole;
+    const bool more = c + 1 < chunks;
     ok = mbar_wait(&bb.y_full, ph, err, abort_flag) && ok;
-    if (!kStateOnly && t == 0 && ok && (ok = mbar_wait(&bb.x_full, ph, err, abort_flag))) {
-      constexpr uint32_t id_a = idesc_bf16(128, 64, 0, 0);
-      const uint64_t yd = desc_kmajor_base(smem_u32(smem + L::kY)),
-                     xd = desc_kmajor_base(smem_u32(smem + L::kX));
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        mma_ss(tmem + 128, desc_advance(yd, kmajor_step_bytes(64, ks)),
-               desc_advance(xd, kmajor_step_bytes(64, ks)), id_a, ks > 0);
-      mma_commit(&bb.a_done);
-    }
     if (ok) {
       // w y in three bf16 parts; rows behind the piece are 0
 #pragma unroll
@@ -191,55 +216,28 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
         *reinterpret_cast<uint4*>(dst + 2 * L::kT) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
       }
     }
-    // the state: rounded for the products, decayed for the sum
-    uint32_t sb[kHalf / 2];
-#pragma unroll
-    for (int c0 = 0; c0 < kHalf; c0 += 32) {
-      float v[32];
-      tmem_ld32(tS + c0, v);
-      tmem_ld_wait();
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sb[c0 / 2 + e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(scaled(v[q * 16 + e], carry));
-        tmem_st16(tS + c0 + q * 16, w);
-      }
-    }
     if (!kStateOnly) {
       ok = ok && mbar_wait(&bb.a_done, ph, err, abort_flag);
       tc_fence_after();
-      if (ok) {
-        // a warp reads A and writes S in the same 32 columns of its own lanes
-        if ((warp & 3) < 2) {
-          const int s = z;
-          float v[32];
-          tmem_ld32(tA + wg * 32, v);
-          tmem_ld_wait();
+      if (ok && (warp & 3) < 2) {
+        const int s = z;
+        float v[32];
+        tmem_ld32(tA + wg * 32, v);
+        tmem_ld_wait();
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t p[4];
+        for (int u = 0; u < 4; ++u) {
+          uint32_t p[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float f[2];
+          for (int k = 0; k < 4; ++k) {
+            float f[2];
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int e = u * 8 + k * 2 + q, n = rev ? s - (wg * 32 + e) : wg * 32 + e - s;
-                f[q] = n >= 0 && s < r ? v[e] * (g.f_intra * pw[n < 0 ? 0 : n]) : 0.f;
-              }
-              p[k] = pack_bf16(f[0], f[1]);
+            for (int q = 0; q < 2; ++q) {
+              const int e = u * 8 + k * 2 + q, n = rev ? s - (wg * 32 + e) : wg * 32 + e - s;
+              f[q] = n >= 0 && s < r ? v[e] * (g.f_intra * pw[n < 0 ? 0 : n]) : 0.f;
             }
-            st_sw128_unit(smem + L::kP, 64, s, wg * 32 + u * 8, make_uint4(p[0], p[1], p[2], p[3]));
+            p[k] = pack_bf16(f[0], f[1]);
           }
-        }
-#pragma unroll
-        for (int q = 0; q < kHalf / 2; q += 16) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = sb[q + e];
-          tmem_st16(tA + wg * 32 + q, w);
+          st_sw128_unit(smem + L::kP, 64, s, wg * 32 + u * 8, make_uint4(p[0], p[1], p[2], p[3]));
         }
       }
     }
@@ -250,47 +248,36 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
         for (int b = r * 128 + t * 16; b < 8192; b += 4096)
           *reinterpret_cast<uint4*>(smem + L::kZ + k * 8192 + b) = make_uint4(0, 0, 0, 0);
     }
-    tmem_st_wait();
     fence_proxy_async_smem();
     tc_fence_before();
     ok = __syncthreads_and(ok);
     tc_fence_after();
     if (!ok) break;
     if (t == 0) {
-      const bool more = c + 1 < chunks;
       if (more) load(tm_y, L::kY, &bb.y_full, c + 1);
-      constexpr uint32_t id_o1 = idesc_bf16(128, 64, 0, 0), id_o2 = idesc_bf16(128, 64, 1, 1),
-                         id_u = idesc_bf16(128, D, 1, 1);
+      if (more && !kStateOnly) load(tm_x, L::kX, &bb.x_full, c + 1);
+      constexpr uint32_t id_o2 = idesc_bf16(128, 64, 1, 1), id_u = idesc_bf16(128, D, 1, 1);
       const uint64_t zd = desc_mnmajor_base(smem_u32(smem + L::kZ), 64);
+      ok = mbar_wait(&bb.z_full, ph, err, abort_flag);
+      tc_fence_after();
       if (!kStateOnly) {
-        const uint64_t xd = desc_kmajor_base(smem_u32(smem + L::kX)),
-                       pd = desc_mnmajor_base(smem_u32(smem + L::kP), 64);
-        constexpr int kPer = D / 32;  // k-steps of a warpgroup's half of the state
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_ts(tmem + 192, tmem + 128 + (ks / kPer) * 32 + (ks % kPer) * 8,
-                 desc_advance(xd, kmajor_step_bytes(64, ks)), id_o1, ks > 0);
-        ok = mbar_wait(&bb.z_full, ph, err, abort_flag);
+        const uint64_t pd = desc_mnmajor_base(smem_u32(smem + L::kP), 64);
         if (ok) {
-          tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             mma_ss(tmem + 128, desc_advance(zd, mnmajor_step_bytes(ks)),
                    desc_advance(pd, mnmajor_step_bytes(ks)), id_o2, ks > 0);
         }
         mma_commit(&bb.o_done);
-      } else {
-        ok = mbar_wait(&bb.z_full, ph, err, abort_flag);
-        tc_fence_after();
       }
       if (ok) {
 #pragma unroll
-        for (int q = 0; q < 3; ++q) {
+        for (int q = 2; q >= 0; --q) {  // the small parts first
           const uint64_t yd = desc_mnmajor_base(smem_u32(smem + L::kYs + q * L::kT), 64);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             mma_ss(tmem, desc_advance(zd, mnmajor_step_bytes(ks)),
-                   desc_advance(yd, mnmajor_step_bytes(ks)), id_u, 1);
+                   desc_advance(yd, mnmajor_step_bytes(ks)), id_u, q < 2 || ks > 0);
         }
       }
       mma_commit(&bb.u_done);
@@ -299,31 +286,46 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
     if (!kStateOnly) {
       ok = mbar_wait(&bb.o_done, ph, err, abort_flag) && ok;
       tc_fence_after();
-      if (t == 0 && ok && c + 1 < chunks) load(tm_x, L::kX, &bb.x_full, c + 1);
-      __syncwarp();
       if (ok && (warp & 3) * 32 < D) {
-        float o1[32], o2[32];
-        tmem_ld32(tO1 + wg * 32, o1);
-        tmem_ld32(tA + wg * 32, o2);
-        tmem_ld_wait();
         __nv_bfloat16* dst =
             g.r.out.p + (size_t(pc.row) + row0 + wg * 32) * g.r.out.row + h * g.r.out.head + z;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int k = wg * 32 + e;
-          if (k < r)
-            dst[e * g.r.out.row] =
-                __float2bfloat16(fmaf(o1[e], g.f_inter * pw[rev ? r - 1 - k : k + 1], o2[e]));
+        for (int c0 = 0; c0 < 32; c0 += 16) {
+          float o1[16], o2[16];
+          tmem_ld16(tO1 + wg * 32 + c0, o1);
+          tmem_ld16(tA + wg * 32 + c0, o2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int k = wg * 32 + c0 + e;
+            if (k < r)
+              *dst = __float2bfloat16(fmaf(o1[e], g.f_inter * pw[rev ? r - 1 - k : k + 1], o2[e]));
+            dst += g.r.out.row;
+          }
         }
       }
     }
     ok = mbar_wait(&bb.u_done, ph, err, abort_flag) && ok;
     tc_fence_after();
-    if (t == 0 && ok && c + 1 < chunks) load(tm_z, L::kZ, &bb.z_full, c + 1);
+    if (t == 0 && ok && more) load(tm_z, L::kZ, &bb.z_full, c + 1);
+    __syncwarp();
+    // S = w_r S + U
+    const Factor carry = r < 64 ? decay_factor(gl, r) : whole;
+#pragma unroll
+    for (int c0 = 0; c0 < kHalf; c0 += 16) {
+      float v[16];
+      tmem_ld16(tU + c0, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) S[c0 + e] = scaled(S[c0 + e], carry) + v[e];
+    }
+    if (!kStateOnly && more) put_state();
     tc_fence_before();
     ok = __syncthreads_and(ok);
     tc_fence_after();
     if (!ok) break;
+    if (!kStateOnly && more && t == 0) ok = issue_ao(c + 1);
+    __syncwarp();
   }
 
   if (!ok) {
@@ -340,15 +342,9 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
   } else if (kStateOnly || (g.r.state_out && (rev ? pc.first : pc.last))) {
     float* dst = kStateOnly ? g.states + (size_t(pc.slot) * g.H + h) * D * D
                             : g.r.state_out + (size_t(pc.seq) * g.H + h) * D * D;
-#pragma unroll 1
-    for (int c0 = 0; c0 < kHalf; c0 += 16) {
-      float v[16];
-      tmem_ld16(tS + c0, v);
-      tmem_ld_wait();
-      if (z < D) {
+if (z < D) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) dst[size_t(wg * kHalf + c0 + e) * D + z] = v[e];
-      }
+      for (int e = 0; e < kHalf; ++e) dst[size_t(wg * kHalf + e) * D + z] = S[e];
     }
   }
   tc_fence_before();
@@ -378,15 +374,26 @@ __global__ void __launch_bounds__(256) decay_scan_kernel(const int* __restrict__
                                 p[(z + 3) * D + y])
                   : *reinterpret_cast<const float4*>(p + e);
   }
-  for (int j = 0; j < sp.pieces; ++j) {
+  const auto at = [&](int j) {
     const int k = r.reverse ? sp.pieces - 1 - j : j;
-    float4* at = reinterpret_cast<float4*>(states + (size_t(sp.slot + k) * H + h) * D * D + e);
-    const bool last = j == sp.pieces - 1;
-    const float4 u = last ? s : *at;
-    *at = s;
-    const Factor f = k == sp.pieces - 1 ? part : full;
-    s = make_float4(scaled(s.x, f) + u.x, scaled(s.y, f) + u.y, scaled(s.z, f) + u.z,
-                    scaled(s.w, f) + u.w);
+    return reinterpret_cast<float4*>(states + (size_t(sp.slot + k) * H + h) * D * D + e);
+  };
+  constexpr int kBatch = 8;  // sums in flight (38 us with one, see the run's figures)
+  for (int j0 = 0; j0 < sp.pieces; j0 += kBatch) {
+    float4 u[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (j0 + b < sp.pieces - 1) u[b] = *at(j0 + b);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int j = j0 + b;
+      if (j >= sp.pieces) break;
+      *at(j) = s;
+      if (j == sp.pieces - 1) break;  // nobody asks for the state behind the last piece
+      const Factor f = r.reverse && j == 0 ? part : full;
+      s = make_float4(scaled(s.x, f) + u[b].x, scaled(s.y, f) + u[b].y, scaled(s.z, f) + u[b].z,
+                      scaled(s.w, f) + u[b].w);
+    }
   }
 }
 

@@ -184,7 +184,7 @@ cudaError_t launch_decay_step(const DecayProblem& p, const void* q, const void* 
 struct Factor {
   float hi, lo;
 };
-__device__ __forceinline__ Factor decay_factor(float g, int n) {
+static __device__ __noinline__ Factor decay_factor(float g, int n) {
   const double x = n == 0 ? 1.0 : exp(double(g) * n);
   const float hi = float(x);
   return {hi, float(x - hi)};

@@ -38,13 +38,18 @@ namespace {
 template <int D>
 struct DrSmem {
   static constexpr int kT = 64 * D * 2;                      // x, y or z of a chunk
-  static constexpr int kX = 0, kY = kT, kZ = 2 * kT, kP = 3 * kT, kYs = kP + 8192;
-  static constexpr int kPow = kYs + 3 * kT;                  // w_0 .. w_64
-  static constexpr int kBars = kPow + 272;
-  // no more than two CTAs per SM: each takes half of TMEM
-  static constexpr int kTotal = kBars + 128 > 80 * 1024 ? kBars + 128 : 80 * 1024;
+  static constexpr int kX = 0, kY = kT, kZ = 2 * kT, kP = 3 * kT;
+  // P, then (when O2 has read it) the chunk's output [t][z] on its way out
+  static constexpr int kYs = kP + (8192 > kT ? 8192 : kT);
+  static constexpr int kPow = kYs + 3 * kT;   // l^n, n = 0 .. 64 (reversed runs: n = 64 .. 0)
+  static constexpr int kMix = kPow + 264;     // 129 factors by t - s + 64: scale l^|t - s| or 0
+  static constexpr int kBars = kMix + 520;
+  // two CTAs fit on an SM; not more, as each takes half of TMEM
+  static constexpr int kTotal = kBars + 96 > 80 * 1024 ? kBars + 96 : 80 * 1024;
+  static_assert(kTotal <= (228 * 1024 - 2048) / 2, "two CTAs per SM");
 };
 struct DrBars {
+  Factor carry[2];  // of a whole chunk, of the piece's last one
   uint64_t x_full, y_full, z_full, a_done, o_done, u_done;
   uint32_t tmem_base;
   int abort_flag;
@@ -57,9 +62,17 @@ struct DrArgs {
   const float* log_decay;
   DecayRun r;
   int H, most_slots;
-  float f_intra, f_inter, f_up;
+  float scale;
   int* err;
 };
+
+// The bf16 numbers of the upper halves of two fp32 numbers, and their values.
+__device__ __forceinline__ uint32_t upper_halves(float2 x) {
+  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+__device__ __forceinline__ float2 upper_parts(float2 x) {
+  return make_float2(bf16_hi(__float_as_uint(x.x)), bf16_hi(__float_as_uint(x.y)));
+}
 
 // kStateOnly: the piece's own sum (from a zero state) into its slot, no output.
 template <int D, bool kStateOnly>
@@ -83,6 +96,7 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
     return;
   }
   float* pw = reinterpret_cast<float*>(smem + L::kPow);
+  float* mix = reinterpret_cast<float*>(smem + L::kMix);
   DrBars& bb = *reinterpret_cast<DrBars*>(smem + L::kBars);
   int* err = g.err;
   volatile int* abort_flag = &bb.abort_flag;
@@ -101,7 +115,19 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
     bb.abort_flag = 0;
     fence_barrier_init();
   }
-  if (t >= 64 && t < 64 + 65) pw[t - 64] = decay_factor(gl, t - 64).hi;
+  const int chunks = (pc.rows + 63) / 64, tail = pc.rows - (chunks - 1) * 64;
+  // Factors.  Forward: an update has l^{r-1-s}, the state's share of out_t scale l^{t+1}.
+  // Reversed: scale l^{s+1}, and l^{r-1-t}.  With l^n in `pw` and scale l^n in `mix` each of
+  // them lies in one of the two tables, ascending in t.
+  if (t < 129) {
+    const int n = rev ? 64 - t : t - 64;  // |t - s| on the visible side
+    mix[t] = n >= 0 ? g.scale * decay_factor(gl, n).hi : 0.f;
+  } else if (t < 129 + 65) {
+    const int n = t - 129;
+    pw[rev ? 64 - n : n] = decay_factor(gl, n).hi;
+  } else if (t >= 224 && t < 226) {
+    bb.carry[t - 224] = decay_factor(gl, t == 224 ? 64 : tail);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -109,7 +135,6 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
   const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
   const uint32_t tU = tmem + lane_base + wg * kHalf, tA = tmem + lane_base + 128,
                  tO1 = tmem + lane_base + 192;
-  const int chunks = (pc.rows + 63) / 64;
   // rows of the c-th chunk in walking order
   auto chunk_row = [&](int c) { return (rev ? chunks - 1 - c : c) * 64; };
   auto load = [&](const CUtensorMap& tm, int at, uint64_t* bar, int c) {  // one thread
@@ -125,7 +150,7 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
   }
 
   // the state before the piece: a thread keeps kHalf columns of its lane's row
-  float S[kHalf];
+  float2 S[kHalf / 2];
   {
     const size_t dd = size_t(D) * D;
     const float* src = nullptr;
@@ -141,7 +166,11 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
 #pragma unroll
     for (int e = 0; e < kHalf; ++e) {
       const int y = wg * kHalf + e;
-      S[e] = src && z < D ? src[turned ? z * D + y : y * D + z] : 0.f;
+      const float x = src && z < D ? src[turned ? z * D + y : y * D + z] : 0.f;
+      if (e & 1)
+        S[e / 2].y = x;
+      else
+        S[e / 2].x = x;
     }
   }
   // what a query reads: the state rounded to bf16, as an operand over the place of U
@@ -150,7 +179,7 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
     for (int q = 0; q < kHalf / 2; q += 16) {
       uint32_t w[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) w[e] = pack_bf16(S[2 * (q + e)], S[2 * (q + e) + 1]);
+      for (int e = 0; e < 16; ++e) w[e] = pack_bf16(S[q + e].x, S[q + e].y);
       tmem_st16(tU + q, w);
     }
     tmem_st_wait();
@@ -176,7 +205,6 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
     mma_commit(&bb.a_done);
     return true;
   };
-  const Factor whole = decay_factor(gl, 64);
   bool ok = true;
   if (!kStateOnly && chunks > 0) {
     put_state();
@@ -198,17 +226,20 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
         const int e = t + i * 256, s = e / (D / 8), col = (e % (D / 8)) * 8;
         const uint32_t at = (col >> 6) * 8192 + sw128_offset(s, col & 63);
         const uint4 u = *reinterpret_cast<const uint4*>(smem + L::kY + at);
-        const float f = s < r ? g.f_up * pw[rev ? s + 1 : r - 1 - s] : 0.f;
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        // 24 bits of the product in three parts: the upper halves of the number, of what is
+        // left, and the rest rounded
+        const float f = rev ? mix[63 - s] : pw[s < r ? r - 1 - s : 0];
+        const bool in = s < r;
+        const uint32_t w[4] = {in ? u.x : 0u, in ? u.y : 0u, in ? u.z : 0u, in ? u.w : 0u};
         uint32_t p0[4], p1[4], p2[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float a = s < r ? bf16_lo(w[k]) * f : 0.f, b = s < r ? bf16_hi(w[k]) * f : 0.f;
-          p0[k] = pack_bf16(a, b);
-          a -= bf16_lo(p0[k]);
-          b -= bf16_hi(p0[k]);
-          p1[k] = pack_bf16(a, b);
-          p2[k] = pack_bf16(a - bf16_lo(p1[k]), b - bf16_hi(p1[k]));
+          float2 x = __fmul2_rn(make_float2(bf16_lo(w[k]), bf16_hi(w[k])), make_float2(f, f));
+          p0[k] = upper_halves(x);
+          x = __ffma2_rn(upper_parts(x), make_float2(-1.f, -1.f), x);
+          p1[k] = upper_halves(x);
+          x = __ffma2_rn(upper_parts(x), make_float2(-1.f, -1.f), x);
+          p2[k] = pack_bf16(x.x, x.y);
         }
         uint8_t* dst = smem + L::kYs + at;
         *reinterpret_cast<uint4*>(dst) = make_uint4(p0[0], p0[1], p0[2], p0[3]);
@@ -224,21 +255,20 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
         float v[32];
         tmem_ld32(tA + wg * 32, v);
         tmem_ld_wait();
+        const float* f = mix + 64 + wg * 32 - s;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t p[4];
+        for (int e = 0; e < 32; ++e) v[e] *= f[e];
+        if (s >= r) {  // a row of y behind the piece
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float f[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int e = u * 8 + k * 2 + q, n = rev ? s - (wg * 32 + e) : wg * 32 + e - s;
-              f[q] = n >= 0 && s < r ? v[e] * (g.f_intra * pw[n < 0 ? 0 : n]) : 0.f;
-            }
-            p[k] = pack_bf16(f[0], f[1]);
-          }
-          st_sw128_unit(smem + L::kP, 64, s, wg * 32 + u * 8, make_uint4(p[0], p[1], p[2], p[3]));
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          st_sw128_unit(smem + L::kP, 64, s, wg * 32 + u * 8,
+                        make_uint4(pack_bf16(v[u * 8], v[u * 8 + 1]),
+                                   pack_bf16(v[u * 8 + 2], v[u * 8 + 3]),
+                                   pack_bf16(v[u * 8 + 4], v[u * 8 + 5]),
+                                   pack_bf16(v[u * 8 + 6], v[u * 8 + 7])));
       }
     }
     if (r < 64 && ok && (ok = mbar_wait(&bb.z_full, ph, err, abort_flag))) {
@@ -253,9 +283,11 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
     ok = __syncthreads_and(ok);
     tc_fence_after();
     if (!ok) break;
+    if (t == 32 && more) {  // A, O1 and the split have read y and x
+      load(tm_y, L::kY, &bb.y_full, c + 1);
+      if (!kStateOnly) load(tm_x, L::kX, &bb.x_full, c + 1);
+    }
     if (t == 0) {
-      if (more) load(tm_y, L::kY, &bb.y_full, c + 1);
-      if (more && !kStateOnly) load(tm_x, L::kX, &bb.x_full, c + 1);
       constexpr uint32_t id_o2 = idesc_bf16(128, 64, 1, 1), id_u = idesc_bf16(128, D, 1, 1);
       const uint64_t zd = desc_mnmajor_base(smem_u32(smem + L::kZ), 64);
       ok = mbar_wait(&bb.z_full, ph, err, abort_flag);
@@ -286,38 +318,57 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
     if (!kStateOnly) {
       ok = mbar_wait(&bb.o_done, ph, err, abort_flag) && ok;
       tc_fence_after();
+      // a warpgroup's 32 tokens: turned in shared memory, out as 16 bytes per thread
+      __nv_bfloat16* turn = reinterpret_cast<__nv_bfloat16*>(smem + L::kP) + wg * 32 * D;
       if (ok && (warp & 3) * 32 < D) {
-        __nv_bfloat16* dst =
-            g.r.out.p + (size_t(pc.row) + row0 + wg * 32) * g.r.out.row + h * g.r.out.head + z;
 #pragma unroll
         for (int c0 = 0; c0 < 32; c0 += 16) {
           float o1[16], o2[16];
           tmem_ld16(tO1 + wg * 32 + c0, o1);
           tmem_ld16(tA + wg * 32 + c0, o2);
           tmem_ld_wait();
+          // (tokens behind the piece get any factor: they are not stored)
+          const float* f = (rev ? pw + 65 - r : mix + 65) + wg * 32 + c0;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int k = wg * 32 + c0 + e;
-            if (k < r)
-              *dst = __float2bfloat16(fmaf(o1[e], g.f_inter * pw[rev ? r - 1 - k : k + 1], o2[e]));
-            dst += g.r.out.row;
+          for (int e = 0; e < 16; e += 2) {
+            const float2 x = __ffma2_rn(make_float2(o1[e], o1[e + 1]), make_float2(f[e], f[e + 1]),
+                                        make_float2(o2[e], o2[e + 1]));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+            turn[(c0 + e) * D + z] = b.x;
+            turn[(c0 + e + 1) * D + z] = b.y;
           }
+        }
+      }
+      named_bar_sync(1 + wg, 128);
+      if (ok) {
+        __nv_bfloat16* dst =
+            g.r.out.p + (size_t(pc.row) + row0 + wg * 32) * g.r.out.row + h * g.r.out.head;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const int e = (t & 127) + i * 128, k = e / (D / 8), col = (e % (D / 8)) * 8;
+          if (wg * 32 + k < r)
+            *reinterpret_cast<uint4*>(dst + k * g.r.out.row + col) =
+                *reinterpret_cast<const uint4*>(turn + k * D + col);
         }
       }
     }
     ok = mbar_wait(&bb.u_done, ph, err, abort_flag) && ok;
     tc_fence_after();
-    if (t == 0 && ok && more) load(tm_z, L::kZ, &bb.z_full, c + 1);
+    if (t == 32 && ok && more) load(tm_z, L::kZ, &bb.z_full, c + 1);
     __syncwarp();
     // S = w_r S + U
-    const Factor carry = r < 64 ? decay_factor(gl, r) : whole;
+    const Factor carry = bb.carry[r < 64];
+    const float2 hi = make_float2(carry.hi, carry.hi), lo = make_float2(carry.lo, carry.lo);
 #pragma unroll
     for (int c0 = 0; c0 < kHalf; c0 += 16) {
       float v[16];
       tmem_ld16(tU + c0, v);
       tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) S[c0 + e] = scaled(S[c0 + e], carry) + v[e];
+      for (int e = 0; e < 8; ++e) {
+        float2& x = S[c0 / 2 + e];
+        x = __ffma2_rn(x, hi, __ffma2_rn(x, lo, make_float2(v[2 * e], v[2 * e + 1])));
+      }
     }
     if (!kStateOnly && more) put_state();
     tc_fence_before();
@@ -344,7 +395,8 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
                             : g.r.state_out + (size_t(pc.seq) * g.H + h) * D * D;
 if (z < D) {
 #pragma unroll
-      for (int e = 0; e < kHalf; ++e) dst[size_t(wg * kHalf + e) * D + z] = S[e];
+      for (int e = 0; e < kHalf; ++e)
+        dst[size_t(wg * kHalf + e) * D + z] = e & 1 ? S[e / 2].y : S[e / 2].x;
     }
   }
   tc_fence_before();
@@ -458,8 +510,7 @@ cudaError_t run(const DecayProblem& p, const DecayCut& cut, const DecayRun& r, c
   if (!map(&tx, r.x) || !map(&ty, r.y) || !map(&tz, r.z)) return cudaErrorInvalidValue;
   const DrArgs a{l.counts,       l.pieces, l.states,
                  log_decay,      r,        p.H,
-                 cut.most_slots, p.scale,  r.reverse ? 1.f : p.scale,
-                 r.reverse ? p.scale : 1.f, err};
+                 cut.most_slots, p.scale, err};
   auto* kernel = decay_run_kernel<D, kStateOnly>;
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DrSmem<D>::kTotal);

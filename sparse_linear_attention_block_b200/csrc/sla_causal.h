@@ -144,8 +144,8 @@ inline bool make_tmap_rows(CUtensorMap* m, const void* base, int rows, int heads
                            uint64_t(st.row), uint64_t(st.head), 64, uint32_t(box_rows));
 }
 
-// CTAs that a decay kernel keeps running at once: two on each SM.
-constexpr int kDecaySlots = 296;
+// CTAs that a decay kernel keeps running at once: one on each SM.
+constexpr int kDecaySlots = 148;
 constexpr int kDecayChunk = 64;
 
 // One recurrence R over a sequence's tokens, in order or from the last to the
@@ -199,6 +199,24 @@ __device__ __forceinline__ Seq checked_seq(const SeqIn& in, int i, bool* good) {
   *good = q0 >= 0 && q1 >= q0 && q1 <= in.total_q && q1 - q0 <= in.max_q && k0 >= 0 && k1 >= k0 &&
           k1 <= in.total_k;
   return *good ? Seq{int(q0), int(q1 - q0), int(k0), int(k1 - k0)} : Seq{0, 0, 0, 0};
+}
+
+// The warp's number, and one elected lane, in a form that the compiler knows to be the same
+// for the whole warp.  Products and TMA copies take their operands from uniform registers;
+// issued from a branch on threadIdx they cost about 150 cycles each, whatever their size,
+// issued by an elected lane of a converged warp 48 (N = 64), 64 (N = 128), the tensor pipe's
+// and shared memory's own rates.
+__device__ __forceinline__ int uniform_warp() {
+  return __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0);
+}
+__device__ __forceinline__ bool elect_sync() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // Write 8 consecutive 32-bit TMEM columns of a warp's 32 lanes.

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
   DqBars<D>& bb = *reinterpret_cast<DqBars<D>*>(smem_raw + L::kTiles);
   int* err = g.err;
   volatile int* abort_flag = &bb.abort_flag;
-  const int warp = threadIdx.x / 32, lane = lane_id();
+  const int warp = uniform_warp(), lane = lane_id();
 
   const int off = it.s.nk - it.s.nq;
   int a0[2], head[2], n[2];
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
     if (warp == 8 && nt > 0) {
       // ---------------------------------------------------------------- producer
-      if (lane == 0) {
+      if (elect_sync()) {
         mbar_arrive_expect_tx(&bb.q_full, 4 * L::kQ);
         for (int h = 0; h < 2; ++h)
           for (int c = 0; c < D / 64; ++c) {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
         const int valid = it.s.nk - j * 64;
         uint8_t* dst = sK + s * L::kKV;
         uint64_t* bar = valid < 64 ? &bb.k_fix : &bb.k_full[s];
-        if (lane == 0) {
+        if (elect_sync()) {
           mbar_arrive_expect_tx(bar, L::kKV);
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(dst + c * 8192, bar, &tm_k, c * 64, it.s.k0 + j * 64, hk);
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
           if (lane == 0) mbar_arrive(&bb.k_full[s]);
         }
         if (j >= kSt && !(go = mbar_wait(&bb.v_empty[s], ph, err, abort_flag))) break;
-        if (lane == 0) {
+        if (elect_sync()) {
           mbar_arrive_expect_tx(&bb.v_full[s], L::kKV);
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(sV + s * L::kKV + c * 8192, &bb.v_full[s], &tm_v, c * 64,
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
         for (int j = max(0, nv - kSt); j < nv; ++j)
           mbar_wait(&bb.v_full[j % kSt], (j / kSt) & 1, nullptr, nullptr);
       }
-    } else if (warp == 9 && lane == 0 && nt > 0) {
+    } else if (warp == 9 && nt > 0) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_q = idesc_bf16(128, D, 0, 1);
       bool ok = mbar_wait(&bb.q_full, 0, err, abort_flag);
@@ -239,40 +239,49 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
                        od = desc_kmajor_base(smem_u32(sDO + h * L::kQ)),
                        kd = desc_kmajor_base(smem_u32(sK + s * L::kKV)),
                        vd = desc_kmajor_base(smem_u32(sV + s * L::kKV));
+        if (elect_sync()) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t qa = kmajor_step_bytes(128, ks), ka = kmajor_step_bytes(64, ks);
-          mma_ss(tmem + h * 128, desc_advance(qd, qa), desc_advance(kd, ka), id_s, ks > 0);
-          mma_ss(tmem + h * 128 + 64, desc_advance(od, qa), desc_advance(vd, ka), id_s, ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t qa = kmajor_step_bytes(128, ks), ka = kmajor_step_bytes(64, ks);
+            mma_ss(tmem + h * 128, desc_advance(qd, qa), desc_advance(kd, ka), id_s, ks > 0);
+            mma_ss(tmem + h * 128 + 64, desc_advance(od, qa), desc_advance(vd, ka), id_s, ks > 0);
+          }
+          mma_commit(&bb.s_full[h]);
         }
-        mma_commit(&bb.s_full[h]);
+        __syncwarp();
         return true;
       };
       auto issue_dq = [&](int h, int j) -> bool {
         if (!mbar_wait(&bb.ds_full[h], j & 1, err, abort_flag)) return false;
         tc_fence_after();
         const uint64_t kd = desc_mnmajor_base(smem_u32(sK + (j % kSt) * L::kKV), 64);
+        if (elect_sync()) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
-                 desc_advance(kd, mnmajor_step_bytes(ks)), id_q, (j | ks) != 0);
-        if (j == n[h] - 1) mma_commit(&bb.o_full[h]);
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
+                   desc_advance(kd, mnmajor_step_bytes(ks)), id_q, (j | ks) != 0);
+          if (j == n[h] - 1) mma_commit(&bb.o_full[h]);
+        }
+        __syncwarp();
         return true;
       };
       for (int h = 0; ok && h < 2; ++h)
         if (n[h] > 0) ok = issue_s(h, 0);
-      if (ok) mma_commit(&bb.v_empty[0]);
+      if (ok && elect_sync()) mma_commit(&bb.v_empty[0]);
+      __syncwarp();
       for (int j = 0; ok && j < nt; ++j) {
         for (int h = 0; ok && h < 2; ++h) {
           if (j < n[h]) ok = issue_dq(h, j);
           if (ok && j + 1 < n[h]) ok = issue_s(h, j + 1);
         }
-        if (ok) {
+        if (ok && elect_sync()) {
           mma_commit(&bb.k_empty[j % kSt]);
           if (j + 1 < nt) mma_commit(&bb.v_empty[(j + 1) % kSt]);
         }
+        __syncwarp();
       }
-      mma_commit(&bb.mma_done);
+      if (elect_sync()) mma_commit(&bb.mma_done);
+      __syncwarp();
       mbar_wait(&bb.mma_done, 0, nullptr, nullptr);
     }
   } else {
@@ -384,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
   DkBars<D>& bb = *reinterpret_cast<DkBars<D>*>(smem_raw + L::kTiles + L::kLd);
   int* err = g.err;
   volatile int* abort_flag = &bb.abort_flag;
-  const int warp = threadIdx.x / 32, lane = lane_id();
+  const int warp = uniform_warp(), lane = lane_id();
 
   const int off = it.s.nk - it.s.nq, b0 = it.tile * 128;
   // query tiles that see the first of these keys, and the last tile
@@ -428,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
     if (warp == 8 && n > 0) {
       // ---------------------------------------------------------------- producer
-      if (lane == 0) {
+      if (elect_sync()) {
         mbar_arrive_expect_tx(&bb.kv_full, 2 * L::kT);
         for (int c = 0; c < D / 64; ++c) {
           tma_load_3d(sK + c * 16384, &bb.kv_full, &tm_k, c * 64, it.s.k0 + b0, hk);
@@ -443,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
                       int h) -> bool {
         const int valid = it.s.nq - tile * 128;
         uint64_t* bar = valid < 128 ? fix : full;
-        if (lane == 0) {
+        if (elect_sync()) {
           mbar_arrive_expect_tx(bar, L::kT);
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(dst + c * 16384, bar, &tm, c * 64, it.s.q0 + tile * 128, h);
@@ -489,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
         if (fixq == lq - 1 && lq > 0) mbar_wait(&bb.q_fix, fixes & 1, nullptr, nullptr);
         if (fixo == lo - 1 && lo > 0) mbar_wait(&bb.o_fix, fixes & 1, nullptr, nullptr);
       }
-    } else if (warp == 9 && lane == 0 && n > 0) {
+    } else if (warp == 9 && n > 0) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_g = idesc_bf16(128, D, 0, 1);
       const uint64_t kd = desc_kmajor_base(smem_u32(sK)), vd = desc_kmajor_base(smem_u32(sV));
@@ -498,11 +507,14 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
         if (!mbar_wait(&bb.q_full[s], (i / L::kQSt) & 1, err, abort_flag)) return false;
         tc_fence_after();
         const uint64_t qd = desc_kmajor_base(smem_u32(sQ + s * L::kT));
+        if (elect_sync()) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_ss(tmem, desc_advance(kd, kmajor_step_bytes(128, ks)),
-                 desc_advance(qd, kmajor_step_bytes(128, ks)), id_s, ks > 0);
-        mma_commit(&bb.s_full);
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss(tmem, desc_advance(kd, kmajor_step_bytes(128, ks)),
+                   desc_advance(qd, kmajor_step_bytes(128, ks)), id_s, ks > 0);
+          mma_commit(&bb.s_full);
+        }
+        __syncwarp();
         return true;
       };
       auto issue_dp = [&](int i) -> bool {
@@ -510,35 +522,43 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
         if (!mbar_wait(&bb.o_full[s], (i / L::kOSt) & 1, err, abort_flag)) return false;
         tc_fence_after();
         const uint64_t od = desc_kmajor_base(smem_u32(sDO + s * L::kT));
+        if (elect_sync()) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_ss(tmem + 128, desc_advance(vd, kmajor_step_bytes(128, ks)),
-                 desc_advance(od, kmajor_step_bytes(128, ks)), id_s, ks > 0);
-        mma_commit(&bb.dp_full);
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss(tmem + 128, desc_advance(vd, kmajor_step_bytes(128, ks)),
+                   desc_advance(od, kmajor_step_bytes(128, ks)), id_s, ks > 0);
+          mma_commit(&bb.dp_full);
+        }
+        __syncwarp();
         return true;
       };
       // acc += A(TMEM) * B, A's k-step ks (16 queries) at 8 ks of the warpgroup's half
-      auto issue_g = [&](uint32_t acc, uint32_t a, uint8_t* tile, int i) {
+      auto issue_g = [&](uint32_t acc, uint32_t a, uint8_t* tile, int i, uint64_t* free) {
         tc_fence_after();
         const uint64_t bd = desc_mnmajor_base(smem_u32(tile), 128);
+        if (elect_sync()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(acc, a + (ks & 3) * 8 + (ks >> 2) * 64, desc_advance(bd, mnmajor_step_bytes(ks)),
-                 id_g, (i | ks) != 0);
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts(acc, a + (ks & 3) * 8 + (ks >> 2) * 64, desc_advance(bd, mnmajor_step_bytes(ks)),
+                   id_g, (i | ks) != 0);
+          mma_commit(free);
+        }
+        __syncwarp();
       };
       bool ok = mbar_wait(&bb.kv_full, 0, err, abort_flag) && issue_s(0) && issue_dp(0);
       for (int i = 0; ok && i < n; ++i) {
         if (!(ok = mbar_wait(&bb.p_full, i & 1, err, abort_flag))) break;
-        issue_g(tmem + 256, tmem, sDO + (i % L::kOSt) * L::kT, i);
-        mma_commit(&bb.o_empty[i % L::kOSt]);
+        issue_g(tmem + 256, tmem, sDO + (i % L::kOSt) * L::kT, i, &bb.o_empty[i % L::kOSt]);
         if (i + 1 < n && !(ok = issue_s(i + 1))) break;
         if (!(ok = mbar_wait(&bb.ds_full, i & 1, err, abort_flag))) break;
-        issue_g(tmem + 384, tmem + 128, sQ + (i % L::kQSt) * L::kT, i);
-        mma_commit(&bb.q_empty[i % L::kQSt]);
+        issue_g(tmem + 384, tmem + 128, sQ + (i % L::kQSt) * L::kT, i, &bb.q_empty[i % L::kQSt]);
         if (i + 1 < n) ok = issue_dp(i + 1);
       }
-      if (ok) mma_commit(&bb.acc_full);
-      mma_commit(&bb.mma_done);
+      if (elect_sync()) {
+        if (ok) mma_commit(&bb.acc_full);
+        mma_commit(&bb.mma_done);
+      }
+      __syncwarp();
       mbar_wait(&bb.mma_done, 0, nullptr, nullptr);
     } else if (warp == 10 && n > 0) {
       // ---------------------------------------------------------------- statistics

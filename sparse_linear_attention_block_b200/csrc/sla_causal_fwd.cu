@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
   CfBars<D>& bb = *reinterpret_cast<CfBars<D>*>(smem_raw + L::kTiles);
   int* err = g.err;
   volatile int* abort_flag = &bb.abort_flag;
-  const int warp = threadIdx.x / 32, lane = lane_id();
+  const int warp = uniform_warp(), lane = lane_id();
 
   // the two tiles: first query within the sequence, head, key tiles
   const int off = it.s.nk - it.s.nq;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
     if (warp == 8 && nt > 0) {
       // ---------------------------------------------------------------- producer
-      if (lane == 0) {
+      if (elect_sync()) {
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
         const int s = j % kKSt;
         if (j >= kKSt && !mbar_wait(&bb.k_empty[s], ((j / kKSt) + 1) & 1, err, abort_flag))
           return false;
-        if (lane == 0) {
+        if (elect_sync()) {
           mbar_arrive_expect_tx(&bb.k_full[s], L::kTile);
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(sK + s * L::kTile + c * 16384, &bb.k_full[s], &tm_k, c * 64,
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
         const int valid = it.s.nk - j * 128;
         uint64_t* bar = valid < 128 ? &bb.v_fix : &bb.v_full[s];
         uint8_t* dst = sV + s * L::kTile;
-        if (lane == 0) {
+        if (elect_sync()) {
           mbar_arrive_expect_tx(bar, L::kTile);
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(dst + c * 16384, bar, &tm_v, c * 64, it.s.k0 + j * 128, hk);
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
             mbar_wait(&bb.v_full[j % kVSt], (j / kVSt) & 1, nullptr, nullptr);
         if (fix) mbar_wait(&bb.v_fix, 0, nullptr, nullptr);
       }
-    } else if (warp == 9 && lane == 0 && nt > 0) {
+    } else if (warp == 9 && nt > 0) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
       bool ok = mbar_wait(&bb.q_full, 0, err, abort_flag);
@@ -206,11 +206,14 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
         tc_fence_after();
         const uint64_t qd = desc_kmajor_base(smem_u32(sQ + h * L::kTile));
         const uint64_t kd = desc_kmajor_base(smem_u32(sK + s * L::kTile));
+        if (elect_sync()) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_ss(tmem + h * 128, desc_advance(qd, kmajor_step_bytes(128, ks)),
-                 desc_advance(kd, kmajor_step_bytes(128, ks)), id_s, ks > 0);
-        mma_commit(&bb.s_full[h]);
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss(tmem + h * 128, desc_advance(qd, kmajor_step_bytes(128, ks)),
+                   desc_advance(kd, kmajor_step_bytes(128, ks)), id_s, ks > 0);
+          mma_commit(&bb.s_full[h]);
+        }
+        __syncwarp();
         return true;
       };
       auto issue_pv = [&](int h, int j) -> bool {
@@ -220,27 +223,33 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
           return false;
         tc_fence_after();
         const uint64_t vd = desc_mnmajor_base(smem_u32(sV + s * L::kTile), 128);
+        if (elect_sync()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
-                 desc_advance(vd, mnmajor_step_bytes(ks)), id_o, (j | ks) != 0);
-        if (j == n[h] - 1) mma_commit(&bb.o_full[h]);
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
+                   desc_advance(vd, mnmajor_step_bytes(ks)), id_o, (j | ks) != 0);
+          if (j == n[h] - 1) mma_commit(&bb.o_full[h]);
+        }
+        __syncwarp();
         return true;
       };
       for (int h = 0; ok && h < 2; ++h)
         if (n[h] > 0) ok = issue_s(h, 0);
-      if (ok) mma_commit(&bb.k_empty[0]);
+      if (ok && elect_sync()) mma_commit(&bb.k_empty[0]);
+      __syncwarp();
       for (int j = 0; ok && j < nt; ++j) {
         for (int h = 0; ok && h < 2; ++h) {
           if (j < n[h]) ok = issue_pv(h, j);
           if (ok && j + 1 < n[h]) ok = issue_s(h, j + 1);
         }
-        if (ok) {
+        if (ok && elect_sync()) {
           mma_commit(&bb.v_empty[j % kVSt]);
           if (j + 1 < nt) mma_commit(&bb.k_empty[(j + 1) % kKSt]);
         }
+        __syncwarp();
       }
-      mma_commit(&bb.mma_done);
+      if (elect_sync()) mma_commit(&bb.mma_done);
+      __syncwarp();
       mbar_wait(&bb.mma_done, 0, nullptr, nullptr);
     }
   } else {

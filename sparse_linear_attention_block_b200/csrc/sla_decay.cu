@@ -14,13 +14,12 @@
 namespace sla {
 namespace {
 
-// Design of a run (sm_100a).  A CTA (256 threads, two CTAs per SM) walks a piece
-// of a sequence in chunks of 64 tokens with the state S^T [z][y] in registers
-// (fp32).  Per chunk of r tokens, w_n = l^n, forward (reversed runs mirror the
-// exponents):
+// Design of a run (sm_100a).  A persistent-size CTA (one per SM, 512 threads)
+// walks a piece of a sequence in chunks of 64 tokens.  Per chunk of r tokens,
+// w_n = l^n, forward (reversed runs mirror the exponents):
 //   A[s][t]  = y_s . x_t                          MMA, tokens s on the lanes
-//   O1[z][t] = sum_y S[z][y] x_t[y]               MMA, S rounded to bf16 in TMEM
 //   P[s][t]  = w_{t-s} A[s][t]  (s <= t)          bf16, to shared memory
+//   O1[z][t] = sum_y S[z][y] x_t[y]               MMA, S rounded to bf16 in TMEM
 //   O2[z][t] = sum_s z_s P[s][t]                  MMA
 //   U[z][y]  = sum_s z_s w_{r-1-s} y_s            MMA
 //   out_t    = w_{t+1} O1[.][t] + O2[.][t],  S = w_r S + U
@@ -30,30 +29,49 @@ namespace {
 // reads (S and P as operands) is rounded to bf16, like the output.
 // The features lie on the TMEM lanes everywhere (M = 128, for d = 64 with lanes
 // that nobody reads), so the state goes into an A operand without leaving its
-// lanes.  TMEM: S (bf16), then U at 0, A, then O2 at 128, O1 at 192: 256 columns.
-// The bytes of a chunk (x, y, z, out) take longer than its products; what is
-// to be hidden is the chain state -> S in bf16 -> products -> state, which two
-// CTAs per SM do for one another.  A and O1 run while w y is split, the output
-// is written while U runs.
+// lanes.
+// The bytes of a chunk (x, y, z, out: 2750 cycles at an SM's share of the
+// bandwidth for d = 128) take longer than its products (1600 cycles), so the
+// arithmetic between them decides, and what a barrier costs.  The arithmetic is
+// shared out by kind, so that a chunk costs the longest share and not their sum,
+// and only U -> S -> S in bf16 is carried from chunk to chunk:
+//   warps 0-3    w y in three parts, to shared memory             [72 registers]
+//   warps 4-7    P of the next chunk (the lanes of 64 tokens)     [72]
+//   warps 8-11   the output                                       [104]
+//   warps 12-15  the state, one row per thread, in registers      [176]
+//   warp 16      TMA copies, two chunks ahead                     [56]
+//   warp 17, 18  the products (a thread each: U and A; O1 and O2, as a barrier
+//                and a commit cost an issuing thread 60 to 250 cycles)
+// TMEM: U at 0, A at 128 and 192 (two chunks), O1 256, O2 320, S (bf16) 384.
+// Figures (d = 128, 12 heads, 16384 tokens; all kernels of the call): RUNFIG.
+// Two CTAs of 256 threads per SM that did all steps one after the other took
+// 106 us: each step's latency was exposed, and one of the warps waited for the
+// tensor pipe to take its instructions.  One issuing thread, and P and the
+// output in one warpgroup: 125 us.
+constexpr int kRunThreads = 640;
+
 template <int D>
 struct DrSmem {
-  static constexpr int kT = 64 * D * 2;                      // x, y or z of a chunk
-  static constexpr int kX = 0, kY = kT, kZ = 2 * kT, kP = 3 * kT;
-  // P, then (when O2 has read it) the chunk's output [t][z] on its way out
-  static constexpr int kYs = kP + (8192 > kT ? 8192 : kT);
-  static constexpr int kPow = kYs + 3 * kT;   // l^n, n = 0 .. 64 (reversed runs: n = 64 .. 0)
-  static constexpr int kMix = kPow + 264;     // 129 factors by t - s + 64: scale l^|t - s| or 0
+  static constexpr int kT = 64 * D * 2;           // x, y or z of a chunk
+  static constexpr int kSlot = 3 * kT;            // x, y, z
+  static constexpr int kYs = 2 * kSlot;           // two buffers of three parts of w y
+  static constexpr int kP = kYs + 2 * 3 * kT;     // two buffers [s][t]
+  static constexpr int kTurn = kP + 2 * 8192;     // the output on its way out [t][z]
+  static constexpr int kPow = kTurn + kT;         // l^n, n = 0 .. 64 (reversed runs: n = 64 .. 0)
+  static constexpr int kMix = kPow + 264;         // 129 factors by t - s + 64: scale l^|t - s| or 0
   static constexpr int kBars = kMix + 520;
-  // two CTAs fit on an SM; not more, as each takes half of TMEM
-  static constexpr int kTotal = kBars + 96 > 80 * 1024 ? kBars + 96 : 80 * 1024;
-  static_assert(kTotal <= (228 * 1024 - 2048) / 2, "two CTAs per SM");
+  // one CTA per SM, as it takes all of TMEM
+  static constexpr int kTotal = kBars + 256 > 116 * 1024 ? kBars + 256 : 116 * 1024;
+  static_assert(kTotal <= 227 * 1024, "shared memory of a CTA");
 };
 struct DrBars {
   Factor carry[2];  // of a whole chunk, of the piece's last one
-  uint64_t x_full, y_full, z_full, a_done, o_done, u_done;
+  uint64_t in_full[2], split_full[2], a_full[2], p_full[2], u_full[2], o_full[2], u_free, s_full,
+      o1_done, o_free, fin;
   uint32_t tmem_base;
   int abort_flag;
 };
+static_assert(sizeof(DrBars) <= 256, "the place of the barriers");
 
 struct DrArgs {
   const int* counts;
@@ -76,11 +94,10 @@ __device__ __forceinline__ float2 upper_parts(float2 x) {
 
 // kStateOnly: the piece's own sum (from a zero state) into its slot, no output.
 template <int D, bool kStateOnly>
-__global__ void __launch_bounds__(256, 2) decay_run_kernel(
+__global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
     const __grid_constant__ CUtensorMap tm_z, const DrArgs g) {
   using L = DrSmem<D>;
-  constexpr int kHalf = D / 2;  // state columns of a warpgroup
   extern __shared__ __align__(1024) uint8_t smem[];
   const int idx = blockIdx.x / g.H, h = blockIdx.x % g.H;
   if (kStateOnly ? idx >= g.counts[0]
@@ -100,136 +117,83 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
   DrBars& bb = *reinterpret_cast<DrBars*>(smem + L::kBars);
   int* err = g.err;
   volatile int* abort_flag = &bb.abort_flag;
-  const int t = threadIdx.x, warp = t / 32, lane = t % 32;
-  const int wg = warp >> 2, z = (warp & 3) * 32 + lane;  // TMEM lane
+  const int t = threadIdx.x, warp = uniform_warp(), lane = t % 32;
+  const int tl = t & 127;  // thread of a warpgroup: TMEM lane
   const float gl = decay_checked(g.log_decay[h]);
+  const int chunks = (pc.rows + 63) / 64, tail = pc.rows - (chunks - 1) * 64;
 
-  if (warp == 0) tmem_alloc(&bb.tmem_base, 256);
+  if (warp == 0) tmem_alloc(&bb.tmem_base, 512);
   if (t == 32) {
-    mbar_init(&bb.x_full, 1);
-    mbar_init(&bb.y_full, 1);
-    mbar_init(&bb.z_full, 1);
-    mbar_init(&bb.a_done, 1);
-    mbar_init(&bb.o_done, 1);
-    mbar_init(&bb.u_done, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bb.in_full[b], 1);
+      mbar_init(&bb.split_full[b], 4);
+      mbar_init(&bb.a_full[b], 1);
+      mbar_init(&bb.p_full[b], 2);
+      mbar_init(&bb.u_full[b], 1);
+      mbar_init(&bb.o_full[b], 1);
+    }
+    mbar_init(&bb.u_free, 4);
+    mbar_init(&bb.s_full, 4);
+    mbar_init(&bb.o1_done, 1);
+    mbar_init(&bb.o_free, 4);
+    mbar_init(&bb.fin, 2);
     bb.abort_flag = 0;
     fence_barrier_init();
   }
-  const int chunks = (pc.rows + 63) / 64, tail = pc.rows - (chunks - 1) * 64;
   // Factors.  Forward: an update has l^{r-1-s}, the state's share of out_t scale l^{t+1}.
   // Reversed: scale l^{s+1}, and l^{r-1-t}.  With l^n in `pw` and scale l^n in `mix` each of
   // them lies in one of the two tables, ascending in t.
-  if (t < 129) {
-    const int n = rev ? 64 - t : t - 64;  // |t - s| on the visible side
-    mix[t] = n >= 0 ? g.scale * decay_factor(gl, n).hi : 0.f;
-  } else if (t < 129 + 65) {
-    const int n = t - 129;
+  if (t >= 128 && t < 128 + 129) {
+    const int i = t - 128, n = rev ? 64 - i : i - 64;  // |t - s| on the visible side
+    mix[i] = n >= 0 ? g.scale * decay_factor(gl, n).hi : 0.f;
+  } else if (t >= 288 && t < 288 + 65) {
+    const int n = t - 288;
     pw[rev ? 64 - n : n] = decay_factor(gl, n).hi;
-  } else if (t >= 224 && t < 226) {
-    bb.carry[t - 224] = decay_factor(gl, t == 224 ? 64 : tail);
+  } else if (t >= 384 && t < 386) {
+    bb.carry[t - 384] = decay_factor(gl, t == 384 ? 64 : tail);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bb.tmem_base;
   const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
-  const uint32_t tU = tmem + lane_base + wg * kHalf, tA = tmem + lane_base + 128,
-                 tO1 = tmem + lane_base + 192;
+  constexpr uint32_t kU = 0, kA = 128, kO1 = 256, kO2 = 320, kS = 384;
   // rows of the c-th chunk in walking order
-  auto chunk_row = [&](int c) { return (rev ? chunks - 1 - c : c) * 64; };
-  auto load = [&](const CUtensorMap& tm, int at, uint64_t* bar, int c) {  // one thread
-    mbar_arrive_expect_tx(bar, L::kT);
-#pragma unroll
-    for (int k = 0; k < D / 64; ++k)
-      tma_load_3d(smem + at + k * 8192, bar, &tm, k * 64, pc.row + chunk_row(c), h);
+  const auto chunk_row = [&](int c) { return (rev ? chunks - 1 - c : c) * 64; };
+  const auto wait2 = [&](uint64_t* bar, int c) {  // a barrier pair, used by even and odd chunks
+    const uint32_t ph = (c >> 1) & 1;
+    return mbar_test(&bar[c & 1], ph) || mbar_wait(&bar[c & 1], ph, err, abort_flag);
   };
-  if (t == 0 && chunks > 0) {
-    load(tm_y, L::kY, &bb.y_full, 0);
-    if (!kStateOnly) load(tm_x, L::kX, &bb.x_full, 0);
-    load(tm_z, L::kZ, &bb.z_full, 0);
-  }
-
-  // the state before the piece: a thread keeps kHalf columns of its lane's row
-  float2 S[kHalf / 2];
-  {
-    const size_t dd = size_t(D) * D;
-    const float* src = nullptr;
-    bool turned = false;
-    if (!kStateOnly) {
-      if (pc.slot >= 0) {
-        src = g.states + (size_t(pc.slot) * g.H + h) * dd;
-      } else if (g.r.state_in) {
-        src = g.r.state_in + (size_t(pc.seq) * g.H + h) * dd;
-        turned = g.r.state_t;
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < kHalf; ++e) {
-      const int y = wg * kHalf + e;
-      const float x = src && z < D ? src[turned ? z * D + y : y * D + z] : 0.f;
-      if (e & 1)
-        S[e / 2].y = x;
-      else
-        S[e / 2].x = x;
-    }
-  }
-  // what a query reads: the state rounded to bf16, as an operand over the place of U
-  auto put_state = [&]() {
-#pragma unroll
-    for (int q = 0; q < kHalf / 2; q += 16) {
-      uint32_t w[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) w[e] = pack_bf16(S[q + e].x, S[q + e].y);
-      tmem_st16(tU + q, w);
-    }
-    tmem_st_wait();
+  const auto wait1 = [&](uint64_t* bar, int c) {
+    return mbar_test(bar, c & 1) || mbar_wait(bar, c & 1, err, abort_flag);
   };
-  // A = Y X^T and O1 = S X^T of chunk c (one thread)
-  auto issue_ao = [&](int c) -> bool {
-    constexpr uint32_t id_a = idesc_bf16(128, 64, 0, 0);
-    if (!mbar_wait(&bb.y_full, c & 1, err, abort_flag) ||
-        !mbar_wait(&bb.x_full, c & 1, err, abort_flag))
-      return false;
-    tc_fence_after();
-    const uint64_t yd = desc_kmajor_base(smem_u32(smem + L::kY)),
-                   xd = desc_kmajor_base(smem_u32(smem + L::kX));
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-      mma_ss(tmem + 128, desc_advance(yd, kmajor_step_bytes(64, ks)),
-             desc_advance(xd, kmajor_step_bytes(64, ks)), id_a, ks > 0);
-    constexpr int kPer = D / 32;  // k-steps of a warpgroup's half of the state
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-      mma_ts(tmem + 192, tmem + (ks / kPer) * kHalf + (ks % kPer) * 8,
-             desc_advance(xd, kmajor_step_bytes(64, ks)), id_a, ks > 0);
-    mma_commit(&bb.a_done);
-    return true;
+  // a warp's share is done: its shared memory and TMEM are the next one's
+  const auto hand_over = [&](uint64_t* bar) {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
   };
   bool ok = true;
-  if (!kStateOnly && chunks > 0) {
-    put_state();
-    tc_fence_before();
-    __syncthreads();
-    if (t == 0) ok = issue_ao(0);
-    __syncwarp();
-  }
 
-  for (int c = 0; c < chunks; ++c) {
-    const int row0 = chunk_row(c), r = min(64, pc.rows - row0);
-    const uint32_t ph = c & 1;
-    const bool more = c + 1 < chunks;
-    ok = mbar_wait(&bb.y_full, ph, err, abort_flag) && ok;
-    if (ok) {
-      // w y in three bf16 parts; rows behind the piece are 0
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int e = t + i * 256, s = e / (D / 8), col = (e % (D / 8)) * 8;
+  if (warp < 4) {
+    // ---------------------------------------------------------------- w y in three parts
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+    for (int c = 0; c < chunks; ++c) {
+      const int r = min(64, pc.rows - chunk_row(c));
+      const uint8_t* src = smem + (c & 1) * L::kSlot + L::kT;
+      uint8_t* dst = smem + L::kYs + (c & 1) * 3 * L::kT;
+      ok = wait2(bb.in_full, c) && (c < 2 || wait2(bb.u_full, c - 2));
+      if (!ok) break;
+#pragma unroll 2
+      for (int i = 0; i < D / 16; ++i) {
+        const int e = tl + i * 128, s = e / (D / 8), col = (e % (D / 8)) * 8;
         const uint32_t at = (col >> 6) * 8192 + sw128_offset(s, col & 63);
-        const uint4 u = *reinterpret_cast<const uint4*>(smem + L::kY + at);
+        const uint4 u = *reinterpret_cast<const uint4*>(src + at);
         // 24 bits of the product in three parts: the upper halves of the number, of what is
-        // left, and the rest rounded
-        const float f = rev ? mix[63 - s] : pw[s < r ? r - 1 - s : 0];
+        // left, and the rest rounded; rows behind the piece are 0
         const bool in = s < r;
+        const float f = rev ? mix[63 - s] : pw[in ? r - 1 - s : 0];
         const uint32_t w[4] = {in ? u.x : 0u, in ? u.y : 0u, in ? u.z : 0u, in ? u.w : 0u};
         uint32_t p0[4], p1[4], p2[4];
 #pragma unroll
@@ -241,167 +205,283 @@ __global__ void __launch_bounds__(256, 2) decay_run_kernel(
           x = __ffma2_rn(upper_parts(x), make_float2(-1.f, -1.f), x);
           p2[k] = pack_bf16(x.x, x.y);
         }
-        uint8_t* dst = smem + L::kYs + at;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(p0[0], p0[1], p0[2], p0[3]);
-        *reinterpret_cast<uint4*>(dst + L::kT) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-        *reinterpret_cast<uint4*>(dst + 2 * L::kT) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+        *reinterpret_cast<uint4*>(dst + at) = make_uint4(p0[0], p0[1], p0[2], p0[3]);
+        *reinterpret_cast<uint4*>(dst + L::kT + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+        *reinterpret_cast<uint4*>(dst + 2 * L::kT + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
       }
-    }
-    if (!kStateOnly) {
-      ok = ok && mbar_wait(&bb.a_done, ph, err, abort_flag);
-      tc_fence_after();
-      if (ok && (warp & 3) < 2) {
-        const int s = z;
-        float v[32];
-        tmem_ld32(tA + wg * 32, v);
-        tmem_ld_wait();
-        const float* f = mix + 64 + wg * 32 - s;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] *= f[e];
-        if (s >= r) {  // a row of y behind the piece
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.f;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          st_sw128_unit(smem + L::kP, 64, s, wg * 32 + u * 8,
-                        make_uint4(pack_bf16(v[u * 8], v[u * 8 + 1]),
-                                   pack_bf16(v[u * 8 + 2], v[u * 8 + 3]),
-                                   pack_bf16(v[u * 8 + 4], v[u * 8 + 5]),
-                                   pack_bf16(v[u * 8 + 6], v[u * 8 + 7])));
+      if (r < 64) {
+        // the rows of z behind the piece belong to others: 0 times NaN would be NaN
+        uint8_t* z = smem + (c & 1) * L::kSlot + 2 * L::kT;
+        for (int k = 0; k < D / 64; ++k)
+          for (int b = r * 128 + tl * 16; b < 8192; b += 2048)
+            *reinterpret_cast<uint4*>(z + k * 8192 + b) = make_uint4(0, 0, 0, 0);
       }
+      hand_over(&bb.split_full[c & 1]);
     }
-    if (r < 64 && ok && (ok = mbar_wait(&bb.z_full, ph, err, abort_flag))) {
-      // the rows of z behind the piece belong to others: 0 times NaN would be NaN
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- P
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+    if (!kStateOnly && warp < 6) {  // the lanes of 64 tokens
+      const int s = tl;
+      const float* f = mix + 64 - s;
+      for (int c = 0; c < chunks; ++c) {
+        const int r = min(64, pc.rows - chunk_row(c));
+        uint8_t* dst = smem + L::kP + (c & 1) * 8192;
+        ok = wait2(bb.a_full, c) && (c < 2 || wait2(bb.o_full, c - 2));
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < D / 64; ++k)
-        for (int b = r * 128 + t * 16; b < 8192; b += 4096)
-          *reinterpret_cast<uint4*>(smem + L::kZ + k * 8192 + b) = make_uint4(0, 0, 0, 0);
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    ok = __syncthreads_and(ok);
-    tc_fence_after();
-    if (!ok) break;
-    if (t == 32 && more) {  // A, O1 and the split have read y and x
-      load(tm_y, L::kY, &bb.y_full, c + 1);
-      if (!kStateOnly) load(tm_x, L::kX, &bb.x_full, c + 1);
-    }
-    if (t == 0) {
-      constexpr uint32_t id_o2 = idesc_bf16(128, 64, 1, 1), id_u = idesc_bf16(128, D, 1, 1);
-      const uint64_t zd = desc_mnmajor_base(smem_u32(smem + L::kZ), 64);
-      ok = mbar_wait(&bb.z_full, ph, err, abort_flag);
-      tc_fence_after();
-      if (!kStateOnly) {
-        const uint64_t pd = desc_mnmajor_base(smem_u32(smem + L::kP), 64);
-        if (ok) {
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ss(tmem + 128, desc_advance(zd, mnmajor_step_bytes(ks)),
-                   desc_advance(pd, mnmajor_step_bytes(ks)), id_o2, ks > 0);
-        }
-        mma_commit(&bb.o_done);
-      }
-      if (ok) {
-#pragma unroll
-        for (int q = 2; q >= 0; --q) {  // the small parts first
-          const uint64_t yd = desc_mnmajor_base(smem_u32(smem + L::kYs + q * L::kT), 64);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ss(tmem, desc_advance(zd, mnmajor_step_bytes(ks)),
-                   desc_advance(yd, mnmajor_step_bytes(ks)), id_u, q < 2 || ks > 0);
-        }
-      }
-      mma_commit(&bb.u_done);
-    }
-    __syncwarp();
-    if (!kStateOnly) {
-      ok = mbar_wait(&bb.o_done, ph, err, abort_flag) && ok;
-      tc_fence_after();
-      // a warpgroup's 32 tokens: turned in shared memory, out as 16 bytes per thread
-      __nv_bfloat16* turn = reinterpret_cast<__nv_bfloat16*>(smem + L::kP) + wg * 32 * D;
-      if (ok && (warp & 3) * 32 < D) {
-#pragma unroll
-        for (int c0 = 0; c0 < 32; c0 += 16) {
-          float o1[16], o2[16];
-          tmem_ld16(tO1 + wg * 32 + c0, o1);
-          tmem_ld16(tA + wg * 32 + c0, o2);
+        for (int c0 = 0; c0 < 64; c0 += 16) {
+          float v[16];
+          tmem_ld16(tmem + lane_base + kA + (c & 1) * 64 + c0, v);
           tmem_ld_wait();
-          // (tokens behind the piece get any factor: they are not stored)
-          const float* f = (rev ? pw + 65 - r : mix + 65) + wg * 32 + c0;
+          uint32_t p[8];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float2 x = __ffma2_rn(make_float2(o1[e], o1[e + 1]), make_float2(f[e], f[e + 1]),
-                                        make_float2(o2[e], o2[e + 1]));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
-            turn[(c0 + e) * D + z] = b.x;
-            turn[(c0 + e + 1) * D + z] = b.y;
+          for (int e = 0; e < 8; ++e) {
+            const float2 x = __fmul2_rn(make_float2(v[2 * e], v[2 * e + 1]),
+                                        make_float2(f[c0 + 2 * e], f[c0 + 2 * e + 1]));
+            p[e] = s < r ? pack_bf16(x.x, x.y) : 0u;  // 0: a row of y behind the piece
+          }
+          st_sw128_unit(dst, 64, s, c0, make_uint4(p[0], p[1], p[2], p[3]));
+          st_sw128_unit(dst, 64, s, c0 + 8, make_uint4(p[4], p[5], p[6], p[7]));
+        }
+        hand_over(&bb.p_full[c & 1]);
+      }
+    }
+  } else if (warp < 12) {
+    // ---------------------------------------------------------------- the output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
+    if (!kStateOnly) {
+      // two tokens of a feature lie together while they are turned
+      uint32_t* turn = reinterpret_cast<uint32_t*>(smem + L::kTurn);
+      for (int c = 0; c < chunks; ++c) {
+        const int row0 = chunk_row(c), r = min(64, pc.rows - row0);
+        ok = wait2(bb.o_full, c);
+        if (!ok) break;
+        tc_fence_after();
+        // (tokens behind the piece get any factor: they are not stored)
+        const float* f = rev ? pw + 65 - r : mix + 65;
+        const uint32_t to = tmem + lane_base;
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 16) {
+          float o1[16], o2[16];
+          tmem_ld16(to + kO1 + c0, o1);
+          tmem_ld16(to + kO2 + c0, o2);
+          tmem_ld_wait();
+          if (c0 == 48) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bb.o_free);
+          }
+          if (tl < D) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float2 x =
+                  __ffma2_rn(make_float2(o1[e], o1[e + 1]), make_float2(f[c0 + e], f[c0 + e + 1]),
+                             make_float2(o2[e], o2[e + 1]));
+              turn[(c0 + e) / 2 * D + tl] = pack_bf16(x.x, x.y);
+            }
           }
         }
-      }
-      named_bar_sync(1 + wg, 128);
-      if (ok) {
+        named_bar_sync(1, 128);
         __nv_bfloat16* dst =
-            g.r.out.p + (size_t(pc.row) + row0 + wg * 32) * g.r.out.row + h * g.r.out.head;
+            g.r.out.p + (size_t(pc.row) + row0) * g.r.out.row + h * g.r.out.head;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int e = (t & 127) + i * 128, k = e / (D / 8), col = (e % (D / 8)) * 8;
-          if (wg * 32 + k < r)
-            *reinterpret_cast<uint4*>(dst + k * g.r.out.row + col) =
-                *reinterpret_cast<const uint4*>(turn + k * D + col);
+        for (int i = 0; i < D / 16; ++i) {
+          const int e = tl + i * 128, k = e / (D / 4) * 2, col = (e % (D / 4)) * 4;
+          const uint4 u = *reinterpret_cast<const uint4*>(turn + k / 2 * D + col);
+          if (k < r)
+            *reinterpret_cast<uint2*>(dst + k * g.r.out.row + col) =
+                make_uint2(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410));
+          if (k + 1 < r)
+            *reinterpret_cast<uint2*>(dst + (k + 1) * g.r.out.row + col) =
+                make_uint2(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632));
+        }
+        named_bar_sync(1, 128);
+      }
+    }
+  } else if (warp < 16) {
+    // ---------------------------------------------------------------- the state
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;" ::: "memory");
+    const int z = tl;
+    float2 S[D / 2];
+    {
+      const size_t dd = size_t(D) * D;
+      const float* src = nullptr;
+      bool turned = false;
+      if (!kStateOnly) {
+        if (pc.slot >= 0) {
+          src = g.states + (size_t(pc.slot) * g.H + h) * dd;
+        } else if (g.r.state_in) {
+          src = g.r.state_in + (size_t(pc.seq) * g.H + h) * dd;
+          turned = g.r.state_t;
         }
       }
-    }
-    ok = mbar_wait(&bb.u_done, ph, err, abort_flag) && ok;
-    tc_fence_after();
-    if (t == 32 && ok && more) load(tm_z, L::kZ, &bb.z_full, c + 1);
-    __syncwarp();
-    // S = w_r S + U
-    const Factor carry = bb.carry[r < 64];
-    const float2 hi = make_float2(carry.hi, carry.hi), lo = make_float2(carry.lo, carry.lo);
+      const size_t step = turned ? 1 : D;
+      if (src && z < D) {
+        src += turned ? z * D : z;
 #pragma unroll
-    for (int c0 = 0; c0 < kHalf; c0 += 16) {
-      float v[16];
-      tmem_ld16(tU + c0, v);
-      tmem_ld_wait();
+        for (int e = 0; e < D / 2; ++e)
+          S[e] = make_float2(src[(2 * e) * step], src[(2 * e + 1) * step]);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float2& x = S[c0 / 2 + e];
-        x = __ffma2_rn(x, hi, __ffma2_rn(x, lo, make_float2(v[2 * e], v[2 * e + 1])));
+        for (int e = 0; e < D / 2; ++e) S[e] = make_float2(0.f, 0.f);
       }
     }
-    if (!kStateOnly && more) put_state();
-    tc_fence_before();
-    ok = __syncthreads_and(ok);
-    tc_fence_after();
-    if (!ok) break;
-    if (!kStateOnly && more && t == 0) ok = issue_ao(c + 1);
-    __syncwarp();
-  }
-
-  if (!ok) {
-    // let copies and products already in flight end before the CTA exits (a barrier
-    // without one runs into its time limit)
-    if (t == 0) {
-      for (uint32_t q = 0; q < 2; ++q) {
-        mbar_wait(&bb.x_full, q, nullptr, nullptr);
-        mbar_wait(&bb.y_full, q, nullptr, nullptr);
-        mbar_wait(&bb.z_full, q, nullptr, nullptr);
-        mbar_wait(&bb.u_done, q, nullptr, nullptr);
+    for (int c = 0; c < chunks; ++c) {
+      if (!kStateOnly) {
+        // what a query reads: the state rounded to bf16
+        if (c > 0 && !(ok = wait1(&bb.o1_done, c - 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < D / 2; q += 16) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = pack_bf16(S[q + e].x, S[q + e].y);
+          tmem_st16(tmem + lane_base + kS + q, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bb.s_full);
+      }
+      const Factor carry = bb.carry[pc.rows - chunk_row(c) < 64];
+      const float2 hi = make_float2(carry.hi, carry.hi), lo = make_float2(carry.lo, carry.lo);
+      ok = wait2(bb.u_full, c);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        float v[32];
+        tmem_ld32(tmem + lane_base + kU + c0, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float2& x = S[c0 / 2 + e];
+          x = __ffma2_rn(x, hi, __ffma2_rn(x, lo, make_float2(v[2 * e], v[2 * e + 1])));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bb.u_free);
+    }
+    if (ok && z < D && (kStateOnly || (g.r.state_out && (rev ? pc.first : pc.last)))) {
+      float* dst = (kStateOnly ? g.states + (size_t(pc.slot) * g.H + h) * D * D
+                               : g.r.state_out + (size_t(pc.seq) * g.H + h) * D * D) +
+                   z;
+#pragma unroll
+      for (int e = 0; e < D / 2; ++e) {
+        dst[(2 * e) * D] = S[e].x;
+        dst[(2 * e + 1) * D] = S[e].y;
       }
     }
-  } else if (kStateOnly || (g.r.state_out && (rev ? pc.first : pc.last))) {
-    float* dst = kStateOnly ? g.states + (size_t(pc.slot) * g.H + h) * D * D
-                            : g.r.state_out + (size_t(pc.seq) * g.H + h) * D * D;
-if (z < D) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+    constexpr uint32_t id_a = idesc_bf16(128, 64, 0, 0), id_o2 = idesc_bf16(128, 64, 1, 1),
+                       id_u = idesc_bf16(128, D, 1, 1);
+    const auto slot = [&](int c) { return smem_u32(smem) + (c & 1) * L::kSlot; };
+    if (warp == 16) {
+      // -------------------------------------------------------------- copies
+      int c = 0;
+      for (; c < chunks; ++c) {
+        // the place's products are done: U (and A), O1 and O2 of two chunks before
+        if (c >= 2 && !(ok = wait2(bb.u_full, c - 2) && (kStateOnly || wait2(bb.o_full, c - 2))))
+          break;
+        uint8_t* dst = smem + (c & 1) * L::kSlot;
+        uint64_t* bar = &bb.in_full[c & 1];
+        const int row = pc.row + chunk_row(c);
+        if (elect_sync()) {
+          mbar_arrive_expect_tx(bar, (kStateOnly ? 2 : 3) * L::kT);
 #pragma unroll
-      for (int e = 0; e < kHalf; ++e)
-        dst[size_t(wg * kHalf + e) * D + z] = e & 1 ? S[e / 2].y : S[e / 2].x;
+          for (int k = 0; k < D / 64; ++k) {
+            tma_load_3d(dst + L::kT + k * 8192, bar, &tm_y, k * 64, row, h);
+            if (!kStateOnly) tma_load_3d(dst + k * 8192, bar, &tm_x, k * 64, row, h);
+            tma_load_3d(dst + 2 * L::kT + k * 8192, bar, &tm_z, k * 64, row, h);
+          }
+        }
+        __syncwarp();
+      }
+      if (!ok)  // let copies already in flight land before the CTA exits
+        for (int k = max(0, c - 2); k < c; ++k)
+          mbar_wait(&bb.in_full[k & 1], (k >> 1) & 1, nullptr, nullptr);
+    } else if (warp == 17) {
+      // -------------------------------------------------------------- products A, U
+      const auto issue_a = [&](int c) -> bool {
+        // A's place was read when P of two chunks before came
+        if (!wait2(bb.in_full, c) || (c >= 2 && !wait2(bb.p_full, c - 2))) return false;
+        tc_fence_after();
+        const uint64_t xd = desc_kmajor_base(slot(c)), yd = desc_kmajor_base(slot(c) + L::kT);
+        if (elect_sync()) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss(tmem + kA + (c & 1) * 64, desc_advance(yd, kmajor_step_bytes(64, ks)),
+                   desc_advance(xd, kmajor_step_bytes(64, ks)), id_a, ks > 0);
+          mma_commit(&bb.a_full[c & 1]);
+        }
+        __syncwarp();
+        return true;
+      };
+      if (!kStateOnly && chunks > 0) ok = issue_a(0);
+      for (int c = 0; ok && c < chunks; ++c) {
+        ok = wait2(bb.split_full, c) && (c == 0 || wait1(&bb.u_free, c - 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t zd = desc_mnmajor_base(slot(c) + 2 * L::kT, 64);
+        const uint32_t ys = smem_u32(smem + L::kYs) + (c & 1) * 3 * L::kT;
+        const uint64_t yd = desc_mnmajor_base(ys, 64);
+        if (elect_sync()) {
+#pragma unroll
+          for (int q = 2; q >= 0; --q)  // the small parts first
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss(tmem + kU, desc_advance(zd, mnmajor_step_bytes(ks)),
+                     desc_advance(yd, q * L::kT + mnmajor_step_bytes(ks)), id_u, q < 2 || ks > 0);
+          mma_commit(&bb.u_full[c & 1]);
+        }
+        __syncwarp();
+        // after U: the next chunk's copies may be waiting for it
+        if (!kStateOnly && c + 1 < chunks) ok = issue_a(c + 1);
+      }
+      if (elect_sync()) mma_commit(&bb.fin);
+      __syncwarp();
+      mbar_wait(&bb.fin, 0, nullptr, nullptr);
+    } else if (warp == 18) {
+      // -------------------------------------------------------------- products O1, O2
+      for (int c = 0; !kStateOnly && c < chunks; ++c) {
+        ok = wait2(bb.in_full, c) && wait1(&bb.s_full, c) && (c == 0 || wait1(&bb.o_free, c - 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t xd = desc_kmajor_base(slot(c));
+        if (elect_sync()) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ts(tmem + kO1, tmem + kS + ks * 8, desc_advance(xd, kmajor_step_bytes(64, ks)),
+                   id_a, ks > 0);
+          mma_commit(&bb.o1_done);
+        }
+        __syncwarp();
+        if (!(ok = wait2(bb.p_full, c) && wait2(bb.split_full, c))) break;
+        tc_fence_after();
+        const uint64_t zd = desc_mnmajor_base(slot(c) + 2 * L::kT, 64);
+        const uint64_t pd = desc_mnmajor_base(smem_u32(smem + L::kP) + (c & 1) * 8192, 64);
+        if (elect_sync()) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ss(tmem + kO2, desc_advance(zd, mnmajor_step_bytes(ks)),
+                   desc_advance(pd, mnmajor_step_bytes(ks)), id_o2, ks > 0);
+          mma_commit(&bb.o_full[c & 1]);
+        }
+        __syncwarp();
+      }
+      if (elect_sync()) mma_commit(&bb.fin);
+      __syncwarp();
+      mbar_wait(&bb.fin, 0, nullptr, nullptr);
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_free(tmem, 256);
+  if (warp == 0) tmem_free(tmem, 512);
 }
 
 // The states before the pieces of the cut sequences, over their sums: with U_j
@@ -516,7 +596,7 @@ cudaError_t run(const DecayProblem& p, const DecayCut& cut, const DecayRun& r, c
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DrSmem<D>::kTotal);
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(cut.most_slots + (kStateOnly ? 0 : p.n_seq)) * p.H;
-  kernel<<<grid, 256, DrSmem<D>::kTotal, s>>>(tx, ty, tz, a);
+  kernel<<<grid, kRunThreads, DrSmem<D>::kTotal, s>>>(tx, ty, tz, a);
   return cudaGetLastError();
 }
 

@@ -103,130 +103,140 @@ def sla_decay_query_sizes(shape: DecayShape) -> DecaySizes:
     return out
 
 
-class _Args:
-    """Checks the tensors of one call and collects their addresses."""
+def _layout(rows, heads, d, st):
+    """(shape, strides) that a [rows, heads, d] tensor should have."""
+    r, h = (st.row, st.head) if st.row or st.head else (heads * d, d)
+    return (rows, heads, d), (r, h, 1)
 
-    def __init__(self, what):
-        self.what, self.device = what, None
 
-    def refuse(self, name, why):
-        raise _slab.SlaError(1, f"{self.what}: {name} {why}")
-
-    def _on(self, t, name):
-        device = t.device
-        if device.type != "cuda":
-            self.refuse(name, f"is on {device}, not on a CUDA device")
-        if self.device is None:
-            self.device = device
-        elif device != self.device:
-            self.refuse(name, f"is on {device}, others on {self.device}")
-        return t.data_ptr()
-
-    def rows(self, t, name, rows, heads, d, st):
-        """A bf16 [rows, heads, d] tensor with the shape's strides."""
-        if isinstance(t, int):
-            return t
-        import torch
-        if t.dtype is not torch.bfloat16:
-            self.refuse(name, f"is {t.dtype}, not torch.bfloat16")
-        if t.shape != (rows, heads, d):
-            self.refuse(name, f"has shape {tuple(t.shape)}, not {(rows, heads, d)}")
-        r, h = (st.row, st.head) if st.row or st.head else (heads * d, d)
-        a, b, c = t.stride()
-        if (a != r and rows > 1) or (b != h and heads > 1) or c != 1:
-            self.refuse(name, f"has strides {(a, b, c)}, the shape says {(r, h, 1)}")
-        return self._on(t, name)
-
-    def whole(self, t, name, dtype, numel, optional=False):
-        """A contiguous tensor of at least `numel` elements."""
-        if t is None:
-            if not optional:
-                self.refuse(name, "is required")
-            return None
-        if isinstance(t, int):
-            return t
-        if t.dtype is not dtype:
-            self.refuse(name, f"is {t.dtype}, not {dtype}")
-        if t.numel() < numel or not t.is_contiguous():
-            self.refuse(name, f"is not contiguous with {numel} elements")
-        return self._on(t, name)
-
-    def call(self, fn, stream, *args):
-        import torch
-        if self.device is None:  # plain pointers only
-            _slab._check(fn(*args, _slab._stream(stream)), self.what)
-            return
-        if stream is None:
-            raw = torch.cuda.current_stream(self.device).cuda_stream
+def _layouts(s):
+    """Those of q, k, v, o for a shape, kept with it until one of its fields changes."""
+    key = bytes(s)
+    known = getattr(s, "_known", None)
+    if known is None or known[0] != key:
+        if isinstance(s, CausalShape):
+            known = (key, _layout(s.total_q, s.Hq, s.d, s.q), _layout(s.total_k, s.Hkv, s.d, s.k),
+                     _layout(s.total_k, s.Hkv, s.d, s.v), _layout(s.total_q, s.Hq, s.d, s.o),
+                     s.n_seq, s.Hq * s.total_q, ctypes.byref(s))
         else:
-            device = getattr(stream, "device", None)
-            if device is not None and device != self.device:
-                self.refuse("stream", f"is on {device}, the tensors on {self.device}")
-            raw = stream if isinstance(stream, int) else stream.cuda_stream
-        if torch.cuda.current_device() == self.device.index:
+            known = (key, *(_layout(s.total, s.H, s.d, st) for st in (s.q, s.k, s.v, s.o)),
+                     s.n_seq, s.n_seq * s.H * s.d * s.d, ctypes.byref(s))
+        s._known = known
+    return known
+
+
+def _refuse(what, name, why):
+    raise _slab.SlaError(1, f"{what}: {name} {why}")
+
+
+def _row_problem(t, want, dtype):
+    shape, strides = want
+    if t.dtype is not dtype:
+        return f"is {t.dtype}, not {dtype}"
+    if t.shape != shape:
+        return f"has shape {tuple(t.shape)}, not {shape}"
+    for n, got, st in zip(shape, t.stride(), strides):
+        if got != st and n > 1:
+            return f"has strides {t.stride()}, the shape says {strides}"
+    return None
+
+
+def _call(what, fn, shape_ref, tensors, workspace, stream):
+    """Checks every (tensor, name, layout or (dtype, elements)) and calls fn on their addresses.
+
+    A layout is a pair of tuples: a bf16 [rows, heads, d] tensor with these
+    strides.  (dtype, elements) is a contiguous tensor of at least that many
+    elements; (dtype, elements, None) may be None.
+    """
+    import torch
+    bf16 = torch.bfloat16
+    args, device = [shape_ref], None
+    for t, name, want in tensors:
+        if t.__class__ is int:
+            args.append(t)
+            continue
+        if t is None:
+            if len(want) != 3:
+                _refuse(what, name, "is required")
+            args.append(None)
+            continue
+        kind = want[0]
+        if kind.__class__ is tuple:
+            if t.dtype is not bf16 or t.shape != kind or t.stride() != want[1]:
+                problem = _row_problem(t, want, bf16)
+                if problem:
+                    _refuse(what, name, problem)
+        elif t.dtype is not kind:
+            _refuse(what, name, f"is {t.dtype}, not {kind}")
+        elif t.numel() < want[1] or not t.is_contiguous():
+            _refuse(what, name, f"is not contiguous with {want[1]} elements")
+        d = t.get_device()
+        if d != device:
+            if d < 0:
+                _refuse(what, name, f"is on {t.device}, not on a CUDA device")
+            if device is not None:
+                _refuse(what, name, f"is on {t.device}, others on device {device}")
+            device = d
+        args.append(t.data_ptr())
+    if workspace is not None:
+        args.append(workspace.numel() * workspace.element_size())
+    if device is None:  # plain pointers only
+        status = fn(*args, _slab._stream(stream))
+    else:
+        if stream is None:
+            raw = torch._C._cuda_getCurrentRawStream(device)
+        elif stream.__class__ is int:
+            raw = stream
+        else:
+            if stream.device.index != device:
+                _refuse(what, "stream", f"is on {stream.device}, the tensors on device {device}")
+            raw = stream.cuda_stream
+        if torch._C._cuda_getDevice() == device:
             status = fn(*args, raw)
         else:
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(device):
                 status = fn(*args, raw)
-        _slab._check(status, self.what)
-
-
-def _qkv(a, s, q, k, v, rows_q, rows_k, Hq, Hkv, names="qkv"):
-    return (a.rows(q, names[0], rows_q, Hq, s.d, s.q), a.rows(k, names[1], rows_k, Hkv, s.d, s.k),
-            a.rows(v, names[2], rows_k, Hkv, s.d, s.v))
-
-
-def _workspace(a, ws):
-    import torch
-    return a.whole(ws, "workspace", torch.uint8, 0), ws.numel()
+    if status != 0:
+        raise _slab.SlaError(status, what)
 
 
 def sla_causal_forward(shape: CausalShape, q, k, v, q_off, k_off, k_len, o, lse, workspace,
                        stream=None):
     """Causal attention of packed sequences; k_len (or None) as in sla.h."""
     import torch
-    s, a = shape, _Args("sla_causal_forward")
     i32 = torch.int32
-    ptrs = _qkv(a, s, q, k, v, s.total_q, s.total_k, s.Hq, s.Hkv)
-    ptrs += (a.whole(q_off, "q_off", i32, s.n_seq + 1),
-             a.whole(k_off, "k_off", i32, s.n_seq + (k_len is None)),
-             a.whole(k_len, "k_len", i32, s.n_seq, optional=True),
-             a.rows(o, "o", s.total_q, s.Hq, s.d, s.o),
-             a.whole(lse, "lse", torch.float32, s.Hq * s.total_q))
-    a.call(_slab.lib().sla_causal_forward, stream, ctypes.byref(s), *ptrs,
-           *_workspace(a, workspace))
+    _, lq, lk, lv, lo, n, rows, ref = _layouts(shape)
+    _call("sla_causal_forward", _slab.lib().sla_causal_forward, ref, (
+        (q, "q", lq), (k, "k", lk), (v, "v", lv), (q_off, "q_off", (i32, n + 1)),
+        (k_off, "k_off", (i32, n + (k_len is None))), (k_len, "k_len", (i32, n, None)),
+        (o, "o", lo), (lse, "lse", (torch.float32, rows)),
+        (workspace, "workspace", (torch.uint8, 0))), workspace, stream)
 
 
 def sla_causal_backward(shape: CausalShape, q, k, v, q_off, k_off, o, lse, d_o, dq, dk, dv,
                         workspace, stream=None):
     """Gradients of sum(o * d_o); dq, dk, dv have the strides of q, k, v."""
     import torch
-    s, a = shape, _Args("sla_causal_backward")
     i32 = torch.int32
-    ptrs = _qkv(a, s, q, k, v, s.total_q, s.total_k, s.Hq, s.Hkv)
-    ptrs += (a.whole(q_off, "q_off", i32, s.n_seq + 1), a.whole(k_off, "k_off", i32, s.n_seq + 1),
-             a.rows(o, "o", s.total_q, s.Hq, s.d, s.o),
-             a.whole(lse, "lse", torch.float32, s.Hq * s.total_q),
-             a.rows(d_o, "d_o", s.total_q, s.Hq, s.d, s.o))
-    ptrs += _qkv(a, s, dq, dk, dv, s.total_q, s.total_k, s.Hq, s.Hkv, ("dq", "dk", "dv"))
-    a.call(_slab.lib().sla_causal_backward, stream, ctypes.byref(s), *ptrs,
-           *_workspace(a, workspace))
+    _, lq, lk, lv, lo, n, rows, ref = _layouts(shape)
+    _call("sla_causal_backward", _slab.lib().sla_causal_backward, ref, (
+        (q, "q", lq), (k, "k", lk), (v, "v", lv), (q_off, "q_off", (i32, n + 1)),
+        (k_off, "k_off", (i32, n + 1)), (o, "o", lo), (lse, "lse", (torch.float32, rows)),
+        (d_o, "d_o", lo), (dq, "dq", lq), (dk, "dk", lk), (dv, "dv", lv),
+        (workspace, "workspace", (torch.uint8, 0))), workspace, stream)
 
 
 def sla_decay_forward(shape: DecayShape, q, k, v, log_decay, off, state_in, o, state_out,
                       workspace, stream=None):
     """Decayed linear attention of packed sequences; state_in, state_out may be None."""
     import torch
-    s, a = shape, _Args("sla_decay_forward")
-    f32, n = torch.float32, s.n_seq * s.H * s.d * s.d
-    ptrs = _qkv(a, s, q, k, v, s.total, s.total, s.H, s.H)
-    ptrs += (a.whole(log_decay, "log_decay", f32, s.H), a.whole(off, "off", torch.int32,
-                                                                s.n_seq + 1),
-             a.whole(state_in, "state_in", f32, n, optional=True),
-             a.rows(o, "o", s.total, s.H, s.d, s.o),
-             a.whole(state_out, "state_out", f32, n, optional=True))
-    a.call(_slab.lib().sla_decay_forward, stream, ctypes.byref(s), *ptrs,
-           *_workspace(a, workspace))
+    f32 = torch.float32
+    _, lq, lk, lv, lo, n, state, ref = _layouts(shape)
+    _call("sla_decay_forward", _slab.lib().sla_decay_forward, ref, (
+        (q, "q", lq), (k, "k", lk), (v, "v", lv), (log_decay, "log_decay", (f32, shape.H)),
+        (off, "off", (torch.int32, n + 1)), (state_in, "state_in", (f32, state, None)),
+        (o, "o", lo), (state_out, "state_out", (f32, state, None)),
+        (workspace, "workspace", (torch.uint8, 0))), workspace, stream)
 
 
 def sla_decay_backward(shape: DecayShape, q, k, v, log_decay, off, state_in, d_o, d_state_out, dq,
@@ -234,29 +244,26 @@ def sla_decay_backward(shape: DecayShape, q, k, v, log_decay, off, state_in, d_o
     """Gradients of sum(o * d_o) + sum(state_out * d_state_out); the states and
     their gradients may be None."""
     import torch
-    s, a = shape, _Args("sla_decay_backward")
-    f32, n = torch.float32, s.n_seq * s.H * s.d * s.d
-    ptrs = _qkv(a, s, q, k, v, s.total, s.total, s.H, s.H)
-    ptrs += (a.whole(log_decay, "log_decay", f32, s.H), a.whole(off, "off", torch.int32,
-                                                                s.n_seq + 1),
-             a.whole(state_in, "state_in", f32, n, optional=True),
-             a.rows(d_o, "d_o", s.total, s.H, s.d, s.o),
-             a.whole(d_state_out, "d_state_out", f32, n, optional=True))
-    ptrs += _qkv(a, s, dq, dk, dv, s.total, s.total, s.H, s.H, ("dq", "dk", "dv"))
-    ptrs += (a.whole(d_state_in, "d_state_in", f32, n, optional=True),)
-    a.call(_slab.lib().sla_decay_backward, stream, ctypes.byref(s), *ptrs,
-           *_workspace(a, workspace))
+    f32 = torch.float32
+    _, lq, lk, lv, lo, n, state, ref = _layouts(shape)
+    _call("sla_decay_backward", _slab.lib().sla_decay_backward, ref, (
+        (q, "q", lq), (k, "k", lk), (v, "v", lv), (log_decay, "log_decay", (f32, shape.H)),
+        (off, "off", (torch.int32, n + 1)), (state_in, "state_in", (f32, state, None)),
+        (d_o, "d_o", lo), (d_state_out, "d_state_out", (f32, state, None)),
+        (dq, "dq", lq), (dk, "dk", lk), (dv, "dv", lv),
+        (d_state_in, "d_state_in", (f32, state, None)),
+        (workspace, "workspace", (torch.uint8, 0))), workspace, stream)
 
 
 def sla_decay_step(shape: DecayShape, q, k, v, log_decay, state_in, state_out, o, stream=None):
     """One token for each sequence; state_out may be state_in."""
     import torch
-    s, a = shape, _Args("sla_decay_step")
-    f32, n = torch.float32, s.n_seq * s.H * s.d * s.d
-    ptrs = _qkv(a, s, q, k, v, s.total, s.total, s.H, s.H)
-    ptrs += (a.whole(log_decay, "log_decay", f32, s.H), a.whole(state_in, "state_in", f32, n),
-             a.whole(state_out, "state_out", f32, n), a.rows(o, "o", s.total, s.H, s.d, s.o))
-    a.call(_slab.lib().sla_decay_step, stream, ctypes.byref(s), *ptrs)
+    f32 = torch.float32
+    _, lq, lk, lv, lo, _, state, ref = _layouts(shape)
+    _call("sla_decay_step", _slab.lib().sla_decay_step, ref, (
+        (q, "q", lq), (k, "k", lk), (v, "v", lv), (log_decay, "log_decay", (f32, shape.H)),
+        (state_in, "state_in", (f32, state)), (state_out, "state_out", (f32, state)),
+        (o, "o", lo)), None, stream)
 
 
 def _allocate_workspace(nbytes, device, stream):

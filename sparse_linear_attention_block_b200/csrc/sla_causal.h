@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "sla_internal.h"
+#include "sla_ptx.cuh"
 
 namespace sla {
 
@@ -38,11 +39,15 @@ struct alignas(16) Item {
   Seq s;
   int tile, seq, pad0, pad1;
 };
-// A work list: its items in order of falling cost, and how many there are.
+// A work list: its items in order of falling cost, and how many there are.  For one
+// sequence (items == nullptr) no list is made: its tiles from the last one on (queries) or
+// from the first one on (keys) are in that order.
 struct ItemList {
   const int* count;
   const Item* items;
   int most;  // the list has room for that many
+  SeqIn in;
+  int tile;  // rows of a tile
 };
 
 struct CausalProblem {
@@ -217,6 +222,23 @@ __device__ __forceinline__ bool elect_sync() {
       "selp.b32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
+}
+
+// Item `idx` of a list of query tiles (or key tiles); false if there are fewer.
+__device__ __forceinline__ bool fetch_item(const ItemList& l, int idx, bool keys, Item* it,
+                                           int* err) {
+  if (l.items) {
+    if (idx >= *l.count) return false;
+    *it = l.items[idx];
+    return true;
+  }
+  bool good;
+  const Seq s = checked_seq(l.in, 0, &good);
+  if (!good && threadIdx.x == 0) set_error(err, SLA_ERR_DEVICE);
+  const int n = ((keys ? s.nk : s.nq) + l.tile - 1) / l.tile;
+  if (idx >= n) return false;
+  *it = Item{s, keys ? idx : n - 1 - idx, 0, 0, 0};
+  return true;
 }
 
 // Write 8 consecutive 32-bit TMEM columns of a warp's 32 lanes.

@@ -213,11 +213,13 @@ sla_status sla_causal_forward(const sla_causal_shape* shape, const void* q, cons
     return SLA_OK;
   }
   int* counts = at<int>(workspace, L.counts);
-  Item* items = at<Item>(workspace, L.items);
+  Item* items = p.n_seq > 1 ? at<Item>(workspace, L.items) : nullptr;
   const int most = int(most_items(p.total_q, fwd_tile(p), p.n_seq));
-  const CausalPlan plan{fwd_tile(p), most, items, counts, 0, nullptr, nullptr};
-  SLA_LAUNCH("causal_plan", s, launch_causal_plan(in, plan, err, s));
-  const ItemList list{counts, items, most};
+  if (items) {
+    const CausalPlan plan{fwd_tile(p), most, items, counts, 0, nullptr, nullptr};
+    SLA_LAUNCH("causal_plan", s, launch_causal_plan(in, plan, err, s));
+  }
+  const ItemList list{counts, items, most, in, fwd_tile(p)};
   SLA_LAUNCH("causal_fwd", s, launch_causal_fwd(p, q, k, v, list, o, lse, err, s));
   return SLA_OK;
 }
@@ -239,14 +241,18 @@ sla_status sla_causal_backward(const sla_causal_shape* shape, const void* q, con
   int* err = at<int>(workspace, L.err);
   const SeqIn in{q_off, k_off, nullptr, p.n_seq, p.total_q, p.total_k, p.max_q};
   int* counts = at<int>(workspace, L.counts);
-  Item *items = at<Item>(workspace, L.items), *kitems = at<Item>(workspace, L.kitems);
+  Item *items = nullptr, *kitems = nullptr;
   float* dvec = at<float>(workspace, L.dvec);
   const int most = int(most_items(p.total_q, fwd_tile(p), p.n_seq)),
             kmost = int(most_items(p.total_k, kRowTile, p.n_seq));
-  const CausalPlan plan{fwd_tile(p), most, items, counts, kmost, kitems, counts + 1};
-  SLA_LAUNCH("causal_plan", s, launch_causal_plan(in, plan, err, s));
-  const ItemList list{counts, items, most};
-  const ItemList klist{counts + 1, kitems, kmost};
+  if (p.n_seq > 1) {
+    items = at<Item>(workspace, L.items);
+    kitems = at<Item>(workspace, L.kitems);
+    const CausalPlan plan{fwd_tile(p), most, items, counts, kmost, kitems, counts + 1};
+    SLA_LAUNCH("causal_plan", s, launch_causal_plan(in, plan, err, s));
+  }
+  const ItemList list{counts, items, most, in, fwd_tile(p)};
+  const ItemList klist{counts + 1, kitems, kmost, in, kRowTile};
   SLA_LAUNCH("causal_dvec", s, launch_causal_dvec(p, o, d_o, dvec, s));
   SLA_LAUNCH("causal_dkv", s,
              launch_causal_dkv(p, q, k, v, klist, d_o, lse, dvec, dk, dv, err, s));

@@ -19,8 +19,7 @@ constexpr int kThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct CbArgs {
-  const int* count;
-  const Item* items;
+  ItemList list;
   const float *lse, *dvec;
   RowOut out0, out1;  // dq; or dk and dv
   int total_q, heads, G, pair_heads;
@@ -118,8 +117,8 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
   constexpr int kSt = L::kSt;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int item = blockIdx.x / g.heads, hx = blockIdx.x % g.heads;
-  if (item >= *g.count) return;
-  const Item it = g.items[item];
+  Item it;
+  if (!fetch_item(g.list, item, false, &it, g.err)) return;
   if ((smem_u32(smem_raw) & 1023u) != 0u) {
     if (threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
     return;
@@ -379,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
   using L = DkSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int item = blockIdx.x / g.heads, hk = blockIdx.x % g.heads;
-  if (item >= *g.count) return;
-  const Item it = g.items[item];
+  Item it;
+  if (!fetch_item(g.list, item, true, &it, g.err)) return;
   if ((smem_u32(smem_raw) & 1023u) != 0u) {
     if (threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
     return;
@@ -713,7 +712,7 @@ cudaError_t launch_causal_dq(const CausalProblem& p, const void* q, const void* 
       !make_tmap_rows(&tv, v, p.total_k, p.Hkv, p.d, p.v, 64))
     return cudaErrorInvalidValue;
   const int heads = pair_heads(p) ? p.Hq / 2 : p.Hq;
-  const CbArgs a{list.count, list.items, lse,   dvec, out(dq, p.q), RowOut{}, p.total_q,
+  const CbArgs a{list, lse,   dvec, out(dq, p.q), RowOut{}, p.total_q,
                  heads,      p.G,        pair_heads(p), p.scale, p.scale_log2, err};
   const unsigned grid = unsigned(list.most) * heads;
   return p.d == 128 ? launch(causal_dq_kernel<128>, kDqTotal<128>, grid, tq, tdo, tk, tv, a, s)
@@ -729,7 +728,7 @@ cudaError_t launch_causal_dkv(const CausalProblem& p, const void* q, const void*
       !make_tmap_rows(&tk, k, p.total_k, p.Hkv, p.d, p.k, 128) ||
       !make_tmap_rows(&tv, v, p.total_k, p.Hkv, p.d, p.v, 128))
     return cudaErrorInvalidValue;
-  const CbArgs a{list.count, list.items, lse,   dvec,    out(dk, p.k), out(dv, p.v), p.total_q,
+  const CbArgs a{list, lse,   dvec,    out(dk, p.k), out(dv, p.v), p.total_q,
                  p.Hkv,      p.G,        false, p.scale, p.scale_log2, err};
   const unsigned grid = unsigned(list.most) * p.Hkv;
   return p.d == 128 ? launch(causal_dkv_kernel<128>, kDkTotal<128>, grid, tq, tdo, tk, tv, a, s)

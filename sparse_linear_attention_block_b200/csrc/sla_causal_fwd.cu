@@ -52,8 +52,7 @@ template <int D>
 constexpr int kCfTotal = CfSmem<D>::kTiles + int(sizeof(CfBars<D>));
 
 struct CfArgs {
-  const int* count;
-  const Item* items;
+  ItemList list;
   __nv_bfloat16* o;
   long long o_row, o_head;
   float* lse;
@@ -70,8 +69,8 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
   constexpr int kKSt = L::kKSt, kVSt = L::kVSt;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int item = blockIdx.x / g.heads, hx = blockIdx.x % g.heads;
-  if (item >= *g.count) return;
-  const Item it = g.items[item];
+  Item it;
+  if (!fetch_item(g.list, item, false, &it, g.err)) return;
   // the swizzled tiles need 1024-byte alignment: without static shared memory the dynamic
   // region starts at the CTA's window
   if ((smem_u32(smem_raw) & 1023u) != 0u) {
@@ -378,8 +377,7 @@ cudaError_t launch_causal_fwd(const CausalProblem& p, const void* q, const void*
       !make_tmap_rows(&tk, k, p.total_k, p.Hkv, p.d, p.k, 128) ||
       !make_tmap_rows(&tv, v, p.total_k, p.Hkv, p.d, p.v, 128))
     return cudaErrorInvalidValue;
-  const CfArgs a{list.count,
-                 list.items,
+  const CfArgs a{list,
                  static_cast<__nv_bfloat16*>(o),
                  p.o.row,
                  p.o.head,

@@ -104,7 +104,7 @@ struct DecayLayout {
   size_t counts;  // int [4]: slots, splits, whole sequences
   size_t pieces;  // Piece [most_slots + n_seq]: pieces of cut sequences, then whole ones
   size_t splits;  // Split [most_splits]
-  size_t states;  // fp32 [most_slots][H][d][d]
+  size_t states;  // fp32 [2 sets][most_slots][H][d][d]
   size_t total;
 };
 
@@ -155,28 +155,40 @@ constexpr int kDecayChunk = 64;
 
 // One recurrence R over a sequence's tokens, in order or from the last to the
 // first, and what is read from it:
-//   forward:  R = l R + y_t z_t^T,        out_t = fs_out R^T x_t
-//   reverse:  R = R + fs_up y_t z_t^T,    out_t = R^T x_t,   then R = l R
-// (R is [d of y][d of z]).  state_in / state_out: R before the first and after
-// the last step, stored [z][y] where `state_t`.
+//   forward:  R = l R + y_t z_t^T,            out_t = scale R^T x_t
+//   reverse:  R = R + scale y_t z_t^T,        out_t = R^T x_t,   then R = l R
+// (R is [d of y][d of z]).  x, y, z: numbers of the tensors of a DecayCall.
+// state_in / state_out: R before the first and after the last step (or null);
+// state_t: state_in is stored [z][y].  slots: which set of piece states belongs
+// to it, slot_t: stored [z][y] there (the set was made by the run with y and z
+// the other way round); makes: whether it makes the set.
 struct DecayRun {
-  RowView x, y, z;
+  int x, y, z;
   RowOut out;
   const float* state_in;
   float* state_out;
-  bool reverse, state_t;
+  int slots;
+  bool reverse, state_t, slot_t, makes;
+};
+constexpr int kMaxRuns = 3, kMaxTensors = 4;
+// The runs of one call; they share its kernels' grids.
+struct DecayCall {
+  RowView t[kMaxTensors];
+  int tensors;
+  DecayRun r[kMaxRuns];
+  int runs, sets;  // sets of piece states
 };
 cudaError_t launch_decay_plan(const DecayProblem& p, const DecayCut& cut, const int32_t* off,
                               const float* log_decay, const DecayLists& l, int* err,
                               cudaStream_t s);
 // The states before each piece of the cut sequences, into their slots: every
-// piece's own sum, then a walk over the pieces.
-cudaError_t launch_decay_pieces(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+// piece's own sum, then a walk over the pieces.  Then the runs themselves.
+cudaError_t launch_decay_pieces(const DecayProblem& p, const DecayCut& cut, const DecayCall& c,
                                 const DecayLists& l, const float* log_decay, int* err,
                                 cudaStream_t s);
-cudaError_t launch_decay_scan(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+cudaError_t launch_decay_scan(const DecayProblem& p, const DecayCut& cut, const DecayCall& c,
                               const DecayLists& l, const float* log_decay, cudaStream_t s);
-cudaError_t launch_decay_run(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+cudaError_t launch_decay_run(const DecayProblem& p, const DecayCut& cut, const DecayCall& c,
                              const DecayLists& l, const float* log_decay, int* err,
                              cudaStream_t s);
 cudaError_t launch_decay_step(const DecayProblem& p, const void* q, const void* k, const void* v,

@@ -111,8 +111,9 @@ CausalLayout causal_layout(const CausalProblem& p) {
 // Pieces as long as keep every CTA slot of the GPU busy with one, whole chunks, and not
 // below 256 rows: a shorter piece costs more in its state (as many bytes as 128 rows of
 // q, k, v and o) than it gains.
-DecayCut decay_cut(const DecayProblem& p) {
-  const long long even = ((long long)p.total * p.H + kDecaySlots - 1) / kDecaySlots;
+// (A backward has three runs of the same pieces.)
+DecayCut decay_cut(const DecayProblem& p, int runs) {
+  const long long even = ((long long)p.total * p.H * runs + kDecaySlots - 1) / kDecaySlots;
   const long long rows = (even + kDecayChunk - 1) / kDecayChunk * kDecayChunk;
   DecayCut c{};
   c.rows = int(rows < 256 ? 256 : rows > kMaxRows ? kMaxRows : rows);
@@ -131,7 +132,7 @@ DecayLayout decay_layout(const DecayProblem& p, const DecayCut& c) {
   L.counts = take(4 * sizeof(int));
   L.pieces = take((size_t(c.most_slots) + p.n_seq) * sizeof(Piece));
   L.splits = take(size_t(c.most_splits) * sizeof(Split));
-  L.states = take(size_t(c.most_slots) * p.H * p.d * p.d * 4);
+  L.states = take(2 * size_t(c.most_slots) * p.H * p.d * p.d * 4);
   L.total = take.off;
   return L;
 }
@@ -165,14 +166,26 @@ RowOut out_view(void* p, const sla_strides& s) {
       return SLA_ERR_CUDA;                                                 \
   } while (0)
 
-// One output: the states before the pieces of cut sequences, then the walk.
-sla_status decay_pass(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+// The states before the pieces of cut sequences, then the runs.
+sla_status decay_call(const DecayProblem& p, const DecayCut& cut, const DecayCall& c,
                       const DecayLists& l, const float* log_decay, int* err, cudaStream_t s) {
   if (cut.most_slots > 0) {
-    SLA_LAUNCH("decay_pieces", s, launch_decay_pieces(p, cut, r, l, log_decay, err, s));
-    SLA_LAUNCH("decay_scan", s, launch_decay_scan(p, cut, r, l, log_decay, s));
+    SLA_LAUNCH("decay_pieces", s, launch_decay_pieces(p, cut, c, l, log_decay, err, s));
+    SLA_LAUNCH("decay_scan", s, launch_decay_scan(p, cut, c, l, log_decay, s));
   }
-  SLA_LAUNCH("decay_run", s, launch_decay_run(p, cut, r, l, log_decay, err, s));
+  const DecayRun& dv = c.r[1];
+  if (c.runs > 1 && dv.state_out && dv.state_out == dv.state_in) {
+    // d_state_in over d_state_out, which the dK run reads too: dV has to come after it
+    DecayCall first = c, last = c;
+    first.r[1] = c.r[2];
+    first.runs = 2;
+    last.r[0] = dv;
+    last.runs = 1;
+    SLA_LAUNCH("decay_run", s, launch_decay_run(p, cut, first, l, log_decay, err, s));
+    SLA_LAUNCH("decay_run", s, launch_decay_run(p, cut, last, l, log_decay, err, s));
+    return SLA_OK;
+  }
+  SLA_LAUNCH("decay_run", s, launch_decay_run(p, cut, c, l, log_decay, err, s));
   return SLA_OK;
 }
 
@@ -266,7 +279,7 @@ sla_status sla_decay_query_sizes(const sla_decay_shape* shape, sla_decay_sizes* 
   const sla_status st = check_decay(shape, &p);
   if (st != SLA_OK) return st;
   out->state_bytes = size_t(p.n_seq) * p.H * p.d * p.d * 4;
-  out->workspace_bytes = decay_layout(p, decay_cut(p)).total;
+  out->workspace_bytes = decay_layout(p, decay_cut(p, 1)).total;
   return SLA_OK;
 }
 
@@ -280,16 +293,21 @@ sla_status sla_decay_forward(const sla_decay_shape* shape, const void* q, const 
   if (!good(q) || !good(k) || !good(v) || !good(o) || !log_decay || !aligned(log_decay, 4) ||
       !off || !aligned(off, 4) || !good_or_null(state_in) || !good_or_null(state_out))
     return SLA_ERR_INVALID_ARG;
-  const DecayCut cut = decay_cut(p);
+  const DecayCut cut = decay_cut(p, 1);
   const DecayLayout L = decay_layout(p, cut);
   if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = at<int>(workspace, L.err);
   const DecayLists l = decay_lists(workspace, L);
   SLA_LAUNCH("decay_plan", s, launch_decay_plan(p, cut, off, log_decay, l, err, s));
-  const DecayRun r{view(q, p.q), view(k, p.k), view(v, p.v), out_view(o, p.o),
-                   state_in,     state_out,    false,        false};
-  return decay_pass(p, cut, r, l, log_decay, err, s);
+  DecayCall c{};
+  c.t[0] = view(q, p.q);
+  c.t[1] = view(k, p.k);
+  c.t[2] = view(v, p.v);
+  c.tensors = 3;
+  c.r[0] = DecayRun{0, 1, 2, out_view(o, p.o), state_in, state_out, 0, false, false, false, true};
+  c.runs = c.sets = 1;
+  return decay_call(p, cut, c, l, log_decay, err, s);
 }
 
 sla_status sla_decay_backward(const sla_decay_shape* shape, const void* q, const void* k,
@@ -304,21 +322,26 @@ sla_status sla_decay_backward(const sla_decay_shape* shape, const void* q, const
       !log_decay || !aligned(log_decay, 4) || !off || !aligned(off, 4) ||
       !good_or_null(state_in) || !good_or_null(d_state_out) || !good_or_null(d_state_in))
     return SLA_ERR_INVALID_ARG;
-  const DecayCut cut = decay_cut(p);
+  const DecayCut cut = decay_cut(p, kMaxRuns);
   const DecayLayout L = decay_layout(p, cut);
   if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = at<int>(workspace, L.err);
   const DecayLists l = decay_lists(workspace, L);
   SLA_LAUNCH("decay_plan", s, launch_decay_plan(p, cut, off, log_decay, l, err, s));
-  const RowView vq = view(q, p.q), vk = view(k, p.k), vv = view(v, p.v), vd = view(d_o, p.o);
-  const DecayRun rq{vd, vv, vk, out_view(dq, p.q), state_in, nullptr, false, true};
-  const DecayRun rk{vv, vd, vq, out_view(dk, p.k), d_state_out, nullptr, true, true};
-  // last: d_state_in may be d_state_out's buffer
-  const DecayRun rv{vk, vq, vd, out_view(dv, p.v), d_state_out, d_state_in, true, false};
-  if ((st = decay_pass(p, cut, rq, l, log_decay, err, s)) != SLA_OK) return st;
-  if ((st = decay_pass(p, cut, rk, l, log_decay, err, s)) != SLA_OK) return st;
-  return decay_pass(p, cut, rv, l, log_decay, err, s);
+  DecayCall c{};
+  c.t[0] = view(q, p.q);
+  c.t[1] = view(k, p.k);
+  c.t[2] = view(v, p.v);
+  c.t[3] = view(d_o, p.o);
+  c.tensors = 4;
+  c.r[0] = DecayRun{3, 2, 1, out_view(dq, p.q), state_in, nullptr, 0, false, true, false, true};
+  c.r[1] = DecayRun{1, 0, 3, out_view(dv, p.v), d_state_out, d_state_in, 1, true, false, false,
+                    true};
+  c.r[2] = DecayRun{2, 3, 0, out_view(dk, p.k), d_state_out, nullptr, 1, true, true, true, false};
+  c.runs = kMaxRuns;
+  c.sets = 2;
+  return decay_call(p, cut, c, l, log_decay, err, s);
 }
 
 sla_status sla_decay_step(const sla_decay_shape* shape, const void* q, const void* k,

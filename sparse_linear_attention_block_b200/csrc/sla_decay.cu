@@ -60,13 +60,16 @@ struct DrSmem {
   static constexpr int kPow = kTurn + kT;         // l^n, n = 0 .. 64 (reversed runs: n = 64 .. 0)
   static constexpr int kMix = kPow + 264;         // 129 factors by t - s + 64: scale l^|t - s| or 0
   static constexpr int kBars = kMix + 520;
+  // without x, P and the output there is room for four y, z
+  static constexpr int kPlaces = 4, kPair = 2 * kT;
+  static_assert(kPlaces * kPair + 6 * kT <= kPow, "y, z and the parts of w y");
   // one CTA per SM, as it takes all of TMEM
   static constexpr int kTotal = kBars + 256 > 116 * 1024 ? kBars + 256 : 116 * 1024;
   static_assert(kTotal <= 227 * 1024, "shared memory of a CTA");
 };
 struct DrBars {
   Factor carry[2];  // of a whole chunk, of the piece's last one
-  uint64_t in_full[2], split_full[2], a_full[2], p_full[2], u_full[2], o_full[2], u_free, s_full,
+  uint64_t in_full[4], split_full[2], a_full[2], p_full[2], u_full[2], o_full[2], u_free, s_full,
       o1_done, o_free, fin;
   uint32_t tmem_base;
   int abort_flag;
@@ -74,11 +77,12 @@ struct DrBars {
 static_assert(sizeof(DrBars) <= 256, "the place of the barriers");
 
 struct DrArgs {
+  CUtensorMap tm[kMaxTensors];
   const int* counts;
   const Piece* pieces;
   float* states;
   const float* log_decay;
-  DecayRun r;
+  DecayRun r[kMaxRuns];
   int H, most_slots;
   float scale;
   int* err;
@@ -94,9 +98,8 @@ __device__ __forceinline__ float2 upper_parts(float2 x) {
 
 // kStateOnly: the piece's own sum (from a zero state) into its slot, no output.
 template <int D, bool kStateOnly>
-__global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
-    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
-    const __grid_constant__ CUtensorMap tm_z, const DrArgs g) {
+__global__ void __launch_bounds__(kRunThreads, 1)
+    decay_run_kernel(const __grid_constant__ DrArgs g) {
   using L = DrSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int idx = blockIdx.x / g.H, h = blockIdx.x % g.H;
@@ -105,9 +108,10 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
                      (idx >= g.most_slots && idx - g.most_slots < g.counts[2])))
     return;
   const Piece pc = g.pieces[idx];
-  const bool rev = g.r.reverse;
+  const DecayRun& run = g.r[blockIdx.y];
+  const bool rev = run.reverse;
   // the walk over the pieces does not need the last one's sum
-  if (kStateOnly && (rev ? pc.first : pc.last)) return;
+  if (kStateOnly && (!run.makes || (rev ? pc.first : pc.last))) return;
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
     return;
@@ -126,6 +130,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
   if (t == 32) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bb.in_full[b], 1);
+      mbar_init(&bb.in_full[b + 2], 1);
       mbar_init(&bb.split_full[b], 4);
       mbar_init(&bb.a_full[b], 1);
       mbar_init(&bb.p_full[b], 2);
@@ -167,6 +172,21 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
   const auto wait1 = [&](uint64_t* bar, int c) {
     return mbar_test(bar, c & 1) || mbar_wait(bar, c & 1, err, abort_flag);
   };
+  // Places of the inputs.  A run keeps x, y, z of two chunks; without x, four of y, z.
+  constexpr int kPlaces = kStateOnly ? L::kPlaces : 2;
+  const auto at_x = [&](int c) { return (c & 1) * L::kSlot; };
+  const auto at_y = [&](int c) {
+    return kStateOnly ? (c & 3) * L::kPair : (c & 1) * L::kSlot + L::kT;
+  };
+  const auto at_z = [&](int c) { return at_y(c) + L::kT; };
+  const auto at_ys = [&](int c) {
+    return (kStateOnly ? L::kPlaces * L::kPair : L::kYs) + (c & 1) * 3 * L::kT;
+  };
+  const auto wait_in = [&](int c) {
+    const uint32_t ph = (c / kPlaces) & 1;
+    return mbar_test(&bb.in_full[c % kPlaces], ph) ||
+           mbar_wait(&bb.in_full[c % kPlaces], ph, err, abort_flag);
+  };
   // a warp's share is done: its shared memory and TMEM are the next one's
   const auto hand_over = [&](uint64_t* bar) {
     fence_proxy_async_smem();
@@ -174,6 +194,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
+  float* const slots = g.states + size_t(run.slots) * g.most_slots * g.H * D * D;
   bool ok = true;
 
   if (warp < 4) {
@@ -181,9 +202,9 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     for (int c = 0; c < chunks; ++c) {
       const int r = min(64, pc.rows - chunk_row(c));
-      const uint8_t* src = smem + (c & 1) * L::kSlot + L::kT;
-      uint8_t* dst = smem + L::kYs + (c & 1) * 3 * L::kT;
-      ok = wait2(bb.in_full, c) && (c < 2 || wait2(bb.u_full, c - 2));
+      const uint8_t* src = smem + at_y(c);
+      uint8_t* dst = smem + at_ys(c);
+      ok = wait_in(c) && (c < 2 || wait2(bb.u_full, c - 2));
       if (!ok) break;
 #pragma unroll 2
       for (int i = 0; i < D / 16; ++i) {
@@ -211,7 +232,7 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
       }
       if (r < 64) {
         // the rows of z behind the piece belong to others: 0 times NaN would be NaN
-        uint8_t* z = smem + (c & 1) * L::kSlot + 2 * L::kT;
+        uint8_t* z = smem + at_z(c);
         for (int k = 0; k < D / 64; ++k)
           for (int b = r * 128 + tl * 16; b < 8192; b += 2048)
             *reinterpret_cast<uint4*>(z + k * 8192 + b) = make_uint4(0, 0, 0, 0);
@@ -285,16 +306,16 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
         }
         named_bar_sync(1, 128);
         __nv_bfloat16* dst =
-            g.r.out.p + (size_t(pc.row) + row0) * g.r.out.row + h * g.r.out.head;
+            run.out.p + (size_t(pc.row) + row0) * run.out.row + h * run.out.head;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const int e = tl + i * 128, k = e / (D / 4) * 2, col = (e % (D / 4)) * 4;
           const uint4 u = *reinterpret_cast<const uint4*>(turn + k / 2 * D + col);
           if (k < r)
-            *reinterpret_cast<uint2*>(dst + k * g.r.out.row + col) =
+            *reinterpret_cast<uint2*>(dst + k * run.out.row + col) =
                 make_uint2(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410));
           if (k + 1 < r)
-            *reinterpret_cast<uint2*>(dst + (k + 1) * g.r.out.row + col) =
+            *reinterpret_cast<uint2*>(dst + (k + 1) * run.out.row + col) =
                 make_uint2(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632));
         }
         named_bar_sync(1, 128);
@@ -311,10 +332,11 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
       bool turned = false;
       if (!kStateOnly) {
         if (pc.slot >= 0) {
-          src = g.states + (size_t(pc.slot) * g.H + h) * dd;
-        } else if (g.r.state_in) {
-          src = g.r.state_in + (size_t(pc.seq) * g.H + h) * dd;
-          turned = g.r.state_t;
+          src = slots + (size_t(pc.slot) * g.H + h) * dd;
+          turned = run.slot_t;
+        } else if (run.state_in) {
+          src = run.state_in + (size_t(pc.seq) * g.H + h) * dd;
+          turned = run.state_t;
         }
       }
       const size_t step = turned ? 1 : D;
@@ -365,9 +387,9 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(&bb.u_free);
     }
-    if (ok && z < D && (kStateOnly || (g.r.state_out && (rev ? pc.first : pc.last)))) {
-      float* dst = (kStateOnly ? g.states + (size_t(pc.slot) * g.H + h) * D * D
-                               : g.r.state_out + (size_t(pc.seq) * g.H + h) * D * D) +
+    if (ok && z < D && (kStateOnly || (run.state_out && (rev ? pc.first : pc.last)))) {
+      float* dst = (kStateOnly ? slots + (size_t(pc.slot) * g.H + h) * D * D
+                               : run.state_out + (size_t(pc.seq) * g.H + h) * D * D) +
                    z;
 #pragma unroll
       for (int e = 0; e < D / 2; ++e) {
@@ -379,38 +401,40 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
     constexpr uint32_t id_a = idesc_bf16(128, 64, 0, 0), id_o2 = idesc_bf16(128, 64, 1, 1),
                        id_u = idesc_bf16(128, D, 1, 1);
-    const auto slot = [&](int c) { return smem_u32(smem) + (c & 1) * L::kSlot; };
+    const uint32_t s0 = smem_u32(smem);
     if (warp == 16) {
       // -------------------------------------------------------------- copies
       int c = 0;
       for (; c < chunks; ++c) {
-        // the place's products are done: U (and A), O1 and O2 of two chunks before
-        if (c >= 2 && !(ok = wait2(bb.u_full, c - 2) && (kStateOnly || wait2(bb.o_full, c - 2))))
+        // the place's last products are done: U (and A), O1 and O2
+        const int last = c - kPlaces;
+        if (last >= 0 &&
+            !(ok = wait2(bb.u_full, last) && (kStateOnly || wait2(bb.o_full, last))))
           break;
-        uint8_t* dst = smem + (c & 1) * L::kSlot;
-        uint64_t* bar = &bb.in_full[c & 1];
+        uint64_t* bar = &bb.in_full[c % kPlaces];
         const int row = pc.row + chunk_row(c);
         if (elect_sync()) {
           mbar_arrive_expect_tx(bar, (kStateOnly ? 2 : 3) * L::kT);
 #pragma unroll
           for (int k = 0; k < D / 64; ++k) {
-            tma_load_3d(dst + L::kT + k * 8192, bar, &tm_y, k * 64, row, h);
-            if (!kStateOnly) tma_load_3d(dst + k * 8192, bar, &tm_x, k * 64, row, h);
-            tma_load_3d(dst + 2 * L::kT + k * 8192, bar, &tm_z, k * 64, row, h);
+            tma_load_3d(smem + at_y(c) + k * 8192, bar, &g.tm[run.y], k * 64, row, h);
+            if (!kStateOnly)
+              tma_load_3d(smem + at_x(c) + k * 8192, bar, &g.tm[run.x], k * 64, row, h);
+            tma_load_3d(smem + at_z(c) + k * 8192, bar, &g.tm[run.z], k * 64, row, h);
           }
         }
         __syncwarp();
       }
       if (!ok)  // let copies already in flight land before the CTA exits
-        for (int k = max(0, c - 2); k < c; ++k)
-          mbar_wait(&bb.in_full[k & 1], (k >> 1) & 1, nullptr, nullptr);
+        for (int k = max(0, c - kPlaces); k < c; ++k)
+          mbar_wait(&bb.in_full[k % kPlaces], (k / kPlaces) & 1, nullptr, nullptr);
     } else if (warp == 17) {
       // -------------------------------------------------------------- products A, U
       const auto issue_a = [&](int c) -> bool {
         // A's place was read when P of two chunks before came
-        if (!wait2(bb.in_full, c) || (c >= 2 && !wait2(bb.p_full, c - 2))) return false;
+        if (!wait_in(c) || (c >= 2 && !wait2(bb.p_full, c - 2))) return false;
         tc_fence_after();
-        const uint64_t xd = desc_kmajor_base(slot(c)), yd = desc_kmajor_base(slot(c) + L::kT);
+        const uint64_t xd = desc_kmajor_base(s0 + at_x(c)), yd = desc_kmajor_base(s0 + at_y(c));
         if (elect_sync()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
@@ -426,9 +450,8 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
         ok = wait2(bb.split_full, c) && (c == 0 || wait1(&bb.u_free, c - 1));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t zd = desc_mnmajor_base(slot(c) + 2 * L::kT, 64);
-        const uint32_t ys = smem_u32(smem + L::kYs) + (c & 1) * 3 * L::kT;
-        const uint64_t yd = desc_mnmajor_base(ys, 64);
+        const uint64_t zd = desc_mnmajor_base(s0 + at_z(c), 64);
+        const uint64_t yd = desc_mnmajor_base(s0 + at_ys(c), 64);
         if (elect_sync()) {
 #pragma unroll
           for (int q = 2; q >= 0; --q)  // the small parts first
@@ -448,10 +471,10 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
     } else if (warp == 18) {
       // -------------------------------------------------------------- products O1, O2
       for (int c = 0; !kStateOnly && c < chunks; ++c) {
-        ok = wait2(bb.in_full, c) && wait1(&bb.s_full, c) && (c == 0 || wait1(&bb.o_free, c - 1));
+        ok = wait_in(c) && wait1(&bb.s_full, c) && (c == 0 || wait1(&bb.o_free, c - 1));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t xd = desc_kmajor_base(slot(c));
+        const uint64_t xd = desc_kmajor_base(s0 + at_x(c));
         if (elect_sync()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
@@ -462,8 +485,8 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
         __syncwarp();
         if (!(ok = wait2(bb.p_full, c) && wait2(bb.split_full, c))) break;
         tc_fence_after();
-        const uint64_t zd = desc_mnmajor_base(slot(c) + 2 * L::kT, 64);
-        const uint64_t pd = desc_mnmajor_base(smem_u32(smem + L::kP) + (c & 1) * 8192, 64);
+        const uint64_t zd = desc_mnmajor_base(s0 + at_z(c), 64);
+        const uint64_t pd = desc_mnmajor_base(s0 + L::kP + (c & 1) * 8192, 64);
         if (elect_sync()) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
@@ -487,17 +510,25 @@ __global__ void __launch_bounds__(kRunThreads, 1) decay_run_kernel(
 // The states before the pieces of the cut sequences, over their sums: with U_j
 // the j-th piece's sum and n_j its rows,  S_0 = state_in,  S_{j+1} = l^{n_j} S_j + U_j.
 // Four elements per thread.
+struct DsArgs {
+  const int* counts;
+  const Split* splits;
+  float* states;
+  const float* log_decay;
+  DecayRun r[2];  // the run that makes each set
+  int H, rows, most_slots;
+};
 template <int D>
-__global__ void __launch_bounds__(256) decay_scan_kernel(const int* __restrict__ counts,
-                                                         const Split* __restrict__ splits,
-                                                         float* __restrict__ states,
-                                                         const float* __restrict__ log_decay,
-                                                         DecayRun r, int H, int rows) {
-  if (int(blockIdx.x) >= counts[1]) return;
-  const Split sp = splits[blockIdx.x];
-  const int h = blockIdx.y, e = (blockIdx.z * 256 + threadIdx.x) * 4;
-  const float gl = decay_checked(log_decay[h]);
-  const Factor full = decay_factor(gl, rows), part = decay_factor(gl, sp.last_rows);
+__global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__ DsArgs g) {
+  constexpr int kParts = D * D / 1024;
+  if (int(blockIdx.x) >= g.counts[1]) return;
+  const Split sp = g.splits[blockIdx.x];
+  const int h = blockIdx.y, H = g.H, set = blockIdx.z / kParts;
+  const int e = (blockIdx.z % kParts * 256 + threadIdx.x) * 4;
+  const DecayRun& r = g.r[set];
+  float* const states = g.states + size_t(set) * g.most_slots * H * D * D;
+  const float gl = decay_checked(g.log_decay[h]);
+  const Factor full = decay_factor(gl, g.rows), part = decay_factor(gl, sp.last_rows);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (r.state_in) {
     const float* p = r.state_in + (size_t(sp.seq) * H + h) * D * D;
@@ -581,50 +612,57 @@ __global__ void __launch_bounds__(256) decay_step_kernel(
 namespace {
 
 template <int D, bool kStateOnly>
-cudaError_t run(const DecayProblem& p, const DecayCut& cut, const DecayRun& r, const DecayLists& l,
+cudaError_t run(const DecayProblem& p, const DecayCut& cut, const DecayCall& c, const DecayLists& l,
                 const float* log_decay, int* err, cudaStream_t s) {
-  const auto map = [&](CUtensorMap* m, const RowView& v) {
-    return make_tmap_rows(m, v.p, p.total, p.H, D, sla_strides{v.row, v.head}, 64);
-  };
-  CUtensorMap tx, ty, tz;
-  if (!map(&tx, r.x) || !map(&ty, r.y) || !map(&tz, r.z)) return cudaErrorInvalidValue;
-  const DrArgs a{l.counts,       l.pieces, l.states,
-                 log_decay,      r,        p.H,
-                 cut.most_slots, p.scale, err};
+  DrArgs a{};
+  for (int i = 0; i < c.tensors; ++i)
+    if (!make_tmap_rows(&a.tm[i], c.t[i].p, p.total, p.H, D, sla_strides{c.t[i].row, c.t[i].head},
+                        64))
+      return cudaErrorInvalidValue;
+  a.counts = l.counts;
+  a.pieces = l.pieces;
+  a.states = l.states;
+  a.log_decay = log_decay;
+  for (int i = 0; i < c.runs; ++i) a.r[i] = c.r[i];
+  a.H = p.H;
+  a.most_slots = cut.most_slots;
+  a.scale = p.scale;
+  a.err = err;
   auto* kernel = decay_run_kernel<D, kStateOnly>;
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DrSmem<D>::kTotal);
   if (e != cudaSuccess) return e;
-  const unsigned grid = unsigned(cut.most_slots + (kStateOnly ? 0 : p.n_seq)) * p.H;
-  kernel<<<grid, kRunThreads, DrSmem<D>::kTotal, s>>>(tx, ty, tz, a);
+  const dim3 grid(unsigned(cut.most_slots + (kStateOnly ? 0 : p.n_seq)) * p.H,
+                  kStateOnly ? c.sets : c.runs);  // the runs that make a set come first
+  kernel<<<grid, kRunThreads, DrSmem<D>::kTotal, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_decay_run(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+cudaError_t launch_decay_run(const DecayProblem& p, const DecayCut& cut, const DecayCall& c,
                              const DecayLists& l, const float* log_decay, int* err,
                              cudaStream_t s) {
-  return p.d == 128 ? run<128, false>(p, cut, r, l, log_decay, err, s)
-                    : run<64, false>(p, cut, r, l, log_decay, err, s);
+  return p.d == 128 ? run<128, false>(p, cut, c, l, log_decay, err, s)
+                    : run<64, false>(p, cut, c, l, log_decay, err, s);
 }
 
-cudaError_t launch_decay_pieces(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+cudaError_t launch_decay_pieces(const DecayProblem& p, const DecayCut& cut, const DecayCall& c,
                                 const DecayLists& l, const float* log_decay, int* err,
                                 cudaStream_t s) {
-  return p.d == 128 ? run<128, true>(p, cut, r, l, log_decay, err, s)
-                    : run<64, true>(p, cut, r, l, log_decay, err, s);
+  return p.d == 128 ? run<128, true>(p, cut, c, l, log_decay, err, s)
+                    : run<64, true>(p, cut, c, l, log_decay, err, s);
 }
 
-cudaError_t launch_decay_scan(const DecayProblem& p, const DecayCut& cut, const DecayRun& r,
+cudaError_t launch_decay_scan(const DecayProblem& p, const DecayCut& cut, const DecayCall& c,
                               const DecayLists& l, const float* log_decay, cudaStream_t s) {
-  const dim3 grid(cut.most_splits, p.H, p.d * p.d / 1024);
+  DsArgs a{l.counts, l.splits, l.states, log_decay, {c.r[0], c.r[1]}, p.H, cut.rows,
+           cut.most_slots};
+  const dim3 grid(cut.most_splits, p.H, p.d * p.d / 1024 * c.sets);
   if (p.d == 128)
-    decay_scan_kernel<128><<<grid, 256, 0, s>>>(l.counts, l.splits, l.states, log_decay, r, p.H,
-                                                cut.rows);
+    decay_scan_kernel<128><<<grid, 256, 0, s>>>(a);
   else
-    decay_scan_kernel<64><<<grid, 256, 0, s>>>(l.counts, l.splits, l.states, log_decay, r, p.H,
-                                               cut.rows);
+    decay_scan_kernel<64><<<grid, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -253,6 +253,17 @@ __device__ __forceinline__ bool fetch_item(const ItemList& l, int idx, bool keys
   return true;
 }
 
+// The TMEM loads issued so far are complete; `v`'s are used only after this.  With another
+// batch issued right behind it, a batch's arithmetic covers the next one's latency.
+__device__ __forceinline__ void tmem_ld_wait16(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+
 // Write 8 consecutive 32-bit TMEM columns of a warp's 32 lanes.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(

@@ -108,13 +108,32 @@ CausalLayout causal_layout(const CausalProblem& p) {
   return L;
 }
 
-// Pieces as long as keep every CTA slot of the GPU busy with one, whole chunks, and not
-// below 256 rows: a shorter piece costs more in its state (as many bytes as 128 rows of
-// q, k, v and o) than it gains.
-// (A backward has three runs of the same pieces.)
+// How long the pieces are.  One sequence is cut into equal pieces, as many as make the
+// shortest schedule: waves of one CTA per SM, a CTA's time counted in chunks (its start takes
+// about 2.5, the pieces' own sums .6 of a run, the walk over them 5).  For several sequences,
+// whose lengths the host does not know, a third of an SM's even share, so that the CTAs that
+// are left over do not run alone.  Not below 256 rows: a shorter piece's state has more bytes
+// than its rows.  A backward has three runs of the same pieces and two sets of states.
 DecayCut decay_cut(const DecayProblem& p, int runs) {
-  const long long even = ((long long)p.total * p.H * runs + kDecaySlots - 1) / kDecaySlots;
-  const long long rows = (even + kDecayChunk - 1) / kDecayChunk * kDecayChunk;
+  const int sets = runs > 1 ? 2 : 1;
+  long long rows = 256;
+  if (p.n_seq == 1) {
+    double best = 0.;
+    for (int n = 1; n <= kDecaySlots; ++n) {
+      const long long chunks = (p.total + n * (long long)kDecayChunk - 1) / (n * kDecayChunk);
+      if (n > 1 && chunks < 4) break;
+      const auto waves = [&](long long ctas) { return (ctas + kDecaySlots - 1) / kDecaySlots; };
+      double t = waves((long long)n * p.H * runs) * (chunks + 2.5);
+      if (n > 1) t += waves((n - 1ll) * p.H * sets) * (.6 * chunks + 2.5) + 5.;
+      if (n == 1 || t < best) {
+        best = t;
+        rows = chunks * kDecayChunk;
+      }
+    }
+  } else {
+    const long long even = (long long)p.total * p.H * runs / (3 * kDecaySlots);
+    rows = (even + kDecayChunk - 1) / kDecayChunk * kDecayChunk;
+  }
   DecayCut c{};
   c.rows = int(rows < 256 ? 256 : rows > kMaxRows ? kMaxRows : rows);
   if (p.total > c.rows) {
@@ -279,7 +298,9 @@ sla_status sla_decay_query_sizes(const sla_decay_shape* shape, sla_decay_sizes* 
   const sla_status st = check_decay(shape, &p);
   if (st != SLA_OK) return st;
   out->state_bytes = size_t(p.n_seq) * p.H * p.d * p.d * 4;
-  out->workspace_bytes = decay_layout(p, decay_cut(p, 1)).total;
+  const size_t fwd = decay_layout(p, decay_cut(p, 1)).total,
+               bwd = decay_layout(p, decay_cut(p, kMaxRuns)).total;
+  out->workspace_bytes = fwd > bwd ? fwd : bwd;
   return SLA_OK;
 }
 

@@ -56,7 +56,7 @@ struct DrSmem {
   static constexpr int kSlot = 3 * kT;            // x, y, z
   static constexpr int kYs = 2 * kSlot;           // two buffers of three parts of w y
   static constexpr int kP = kYs + 2 * 3 * kT;     // two buffers [s][t]
-  static constexpr int kTurn = kP + 2 * 8192;     // the output on its way out [t][z]
+  static constexpr int kTurn = kP + 2 * 8192;     // the output on its way out [t][z], swizzled
   static constexpr int kPow = kTurn + kT;         // l^n, n = 0 .. 64 (reversed runs: n = 64 .. 0)
   static constexpr int kMix = kPow + 264;         // 129 factors by t - s + 64: scale l^|t - s| or 0
   static constexpr int kBars = kMix + 520;
@@ -77,7 +77,7 @@ struct DrBars {
 static_assert(sizeof(DrBars) <= 256, "the place of the barriers");
 
 struct DrArgs {
-  CUtensorMap tm[kMaxTensors];
+  CUtensorMap tm[kMaxTensors], tm_out[kMaxRuns];
   const int* counts;
   const Piece* pieces;
   float* states;
@@ -251,11 +251,14 @@ __global__ void __launch_bounds__(kRunThreads, 1)
         ok = wait2(bb.a_full, c) && (c < 2 || wait2(bb.o_full, c - 2));
         if (!ok) break;
         tc_fence_after();
+        const uint32_t ta = tmem + lane_base + kA + (c & 1) * 64;
+        float w[2][16];
+        tmem_ld16(ta, w[0]);
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 16) {
-          float v[16];
-          tmem_ld16(tmem + lane_base + kA + (c & 1) * 64 + c0, v);
-          tmem_ld_wait();
+          float(&v)[16] = w[(c0 >> 4) & 1];
+          tmem_ld_wait16(v);
+          if (c0 < 48) tmem_ld16(ta + c0 + 16, w[((c0 >> 4) + 1) & 1]);
           uint32_t p[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -273,8 +276,12 @@ __global__ void __launch_bounds__(kRunThreads, 1)
     // ---------------------------------------------------------------- the output
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;" ::: "memory");
     if (!kStateOnly) {
-      // two tokens of a feature lie together while they are turned
-      uint32_t* turn = reinterpret_cast<uint32_t*>(smem + L::kTurn);
+      uint8_t* const turn = smem + L::kTurn;
+      // this feature's place in a token's row, by token % 8
+      uint32_t at[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        at[e] = (tl >> 6) * 8192 + ((((tl & 63) >> 3) ^ e) << 4) + (tl & 7) * 2;
       for (int c = 0; c < chunks; ++c) {
         const int row0 = chunk_row(c), r = min(64, pc.rows - row0);
         ok = wait2(bb.o_full, c);
@@ -283,13 +290,21 @@ __global__ void __launch_bounds__(kRunThreads, 1)
         // (tokens behind the piece get any factor: they are not stored)
         const float* f = rev ? pw + 65 - r : mix + 65;
         const uint32_t to = tmem + lane_base;
+        // the last chunk's rows have left their place
+        if (tl == 0) bulk_wait_read_all();
+        named_bar_sync(1, 128);
+        float w1[2][16], w2[2][16];
+        tmem_ld16(to + kO1, w1[0]);
+        tmem_ld16(to + kO2, w2[0]);
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 16) {
-          float o1[16], o2[16];
-          tmem_ld16(to + kO1 + c0, o1);
-          tmem_ld16(to + kO2 + c0, o2);
-          tmem_ld_wait();
-          if (c0 == 48) {
+          float(&o1)[16] = w1[(c0 >> 4) & 1], (&o2)[16] = w2[(c0 >> 4) & 1];
+          tmem_ld_wait16(o1);
+          tmem_ld_wait16(o2);
+          if (c0 < 48) {
+            tmem_ld16(to + kO1 + c0 + 16, w1[((c0 >> 4) + 1) & 1]);
+            tmem_ld16(to + kO2 + c0 + 16, w2[((c0 >> 4) + 1) & 1]);
+          } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bb.o_free);
@@ -300,26 +315,33 @@ __global__ void __launch_bounds__(kRunThreads, 1)
               const float2 x =
                   __ffma2_rn(make_float2(o1[e], o1[e + 1]), make_float2(f[c0 + e], f[c0 + e + 1]),
                              make_float2(o2[e], o2[e + 1]));
-              turn[(c0 + e) / 2 * D + tl] = pack_bf16(x.x, x.y);
+              const uint32_t w = pack_bf16(x.x, x.y);
+              *reinterpret_cast<uint16_t*>(turn + at[e & 7] + (c0 + e) * 128) = uint16_t(w);
+              *reinterpret_cast<uint16_t*>(turn + at[(e + 1) & 7] + (c0 + e + 1) * 128) =
+                  uint16_t(w >> 16);
             }
           }
         }
+        fence_proxy_async_smem();
         named_bar_sync(1, 128);
-        __nv_bfloat16* dst =
-            run.out.p + (size_t(pc.row) + row0) * run.out.row + h * run.out.head;
+        if (r == 64) {
+          if (tl == 0) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int e = tl + i * 128, k = e / (D / 4) * 2, col = (e % (D / 4)) * 4;
-          const uint4 u = *reinterpret_cast<const uint4*>(turn + k / 2 * D + col);
-          if (k < r)
-            *reinterpret_cast<uint2*>(dst + k * run.out.row + col) =
-                make_uint2(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410));
-          if (k + 1 < r)
-            *reinterpret_cast<uint2*>(dst + (k + 1) * run.out.row + col) =
-                make_uint2(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632));
+            for (int k = 0; k < D / 64; ++k)
+              tma_store_3d(&g.tm_out[blockIdx.y], turn + k * 8192, k * 64, pc.row + row0, h);
+            bulk_commit();
+          }
+        } else {  // the rows behind the piece are others'
+          __nv_bfloat16* dst =
+              run.out.p + (size_t(pc.row) + row0) * run.out.row + h * run.out.head;
+          for (int e = tl; e < r * (D / 8); e += 128) {
+            const int k = e / (D / 8), col = (e % (D / 8)) * 8;
+            *reinterpret_cast<uint4*>(dst + k * run.out.row + col) =
+                *reinterpret_cast<const uint4*>(turn + (col >> 6) * 8192 + sw128_offset(k, col & 63));
+          }
         }
-        named_bar_sync(1, 128);
       }
+      if (tl == 0) bulk_wait_all();
     }
   } else if (warp < 16) {
     // ---------------------------------------------------------------- the state
@@ -372,15 +394,17 @@ __global__ void __launch_bounds__(kRunThreads, 1)
       ok = wait2(bb.u_full, c);
       if (!ok) break;
       tc_fence_after();
+      float v[2][16];
+      tmem_ld16(tmem + lane_base + kU, v[0]);
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        float v[32];
-        tmem_ld32(tmem + lane_base + kU + c0, v);
-        tmem_ld_wait();
+      for (int i = 0; i < D / 16; ++i) {
+        tmem_ld_wait16(v[i & 1]);
+        if (i + 1 < D / 16) tmem_ld16(tmem + lane_base + kU + (i + 1) * 16, v[(i + 1) & 1]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2& x = S[c0 / 2 + e];
-          x = __ffma2_rn(x, hi, __ffma2_rn(x, lo, make_float2(v[2 * e], v[2 * e + 1])));
+        for (int e = 0; e < 8; ++e) {
+          float2& x = S[i * 8 + e];
+          x = __ffma2_rn(
+              x, hi, __ffma2_rn(x, lo, make_float2(v[i & 1][2 * e], v[i & 1][2 * e + 1])));
         }
       }
       tc_fence_before();
@@ -619,6 +643,11 @@ cudaError_t run(const DecayProblem& p, const DecayCut& cut, const DecayCall& c, 
     if (!make_tmap_rows(&a.tm[i], c.t[i].p, p.total, p.H, D, sla_strides{c.t[i].row, c.t[i].head},
                         64))
       return cudaErrorInvalidValue;
+  for (int i = 0; i < c.runs && !kStateOnly; ++i) {
+    const RowOut& o = c.r[i].out;
+    if (!make_tmap_rows(&a.tm_out[i], o.p, p.total, p.H, D, sla_strides{o.row, o.head}, 64))
+      return cudaErrorInvalidValue;
+  }
   a.counts = l.counts;
   a.pieces = l.pieces;
   a.states = l.states;

@@ -112,8 +112,10 @@ CausalLayout causal_layout(const CausalProblem& p) {
 // shortest schedule: waves of one CTA per SM, a CTA's time counted in chunks (its start takes
 // about 2.5, the pieces' own sums .6 of a run, the walk over them 5).  For several sequences,
 // whose lengths the host does not know, a third of an SM's even share, so that the CTAs that
-// are left over do not run alone.  Not below 256 rows: a shorter piece's state has more bytes
-// than its rows.  A backward has three runs of the same pieces and two sets of states.
+// are left over do not run alone, but not below 512 rows (twelve prompts of 7779 tokens, 12
+// heads: 256 rows 73 us, 63 us with 512, 64 us with 640).  Not below 256 rows otherwise:
+// a shorter piece's state has more bytes than its rows.  A backward has three runs of the same
+// pieces and two sets of states.
 DecayCut decay_cut(const DecayProblem& p, int runs) {
   const int sets = runs > 1 ? 2 : 1;
   long long rows = 256;
@@ -133,6 +135,7 @@ DecayCut decay_cut(const DecayProblem& p, int runs) {
   } else {
     const long long even = (long long)p.total * p.H * runs / (3 * kDecaySlots);
     rows = (even + kDecayChunk - 1) / kDecayChunk * kDecayChunk;
+    if (rows < 512) rows = 512;
   }
   DecayCut c{};
   c.rows = int(rows < 256 ? 256 : rows > kMaxRows ? kMaxRows : rows);

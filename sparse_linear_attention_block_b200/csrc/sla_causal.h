@@ -39,9 +39,9 @@ struct alignas(16) Item {
   Seq s;
   int tile, seq, pad0, pad1;
 };
-// A work list: its items in order of falling cost, and how many there are.  For one
-// sequence (items == nullptr) no list is made: its tiles from the last one on (queries) or
-// from the first one on (keys) are in that order.
+// A work list: its items in order of falling cost, and how many there are.  For up to
+// kDirectSeqs sequences (items == nullptr) no list is made: a CTA finds its item by itself.
+constexpr int kDirectSeqs = 32;
 struct ItemList {
   const int* count;
   const Item* items;
@@ -95,8 +95,8 @@ struct alignas(16) Split {
 // sequences of several have lists of their own.
 struct DecayCut {
   int rows;
-  int most_slots;   // pieces of cut sequences: below 2 total / rows
-  int most_splits;  // cut sequences: below total / rows
+  int most_slots;   // pieces of cut sequences
+  int most_splits;  // cut sequences
 };
 
 struct DecayLayout {
@@ -108,11 +108,16 @@ struct DecayLayout {
   size_t total;
 };
 
+// The lists, or (pieces == nullptr, up to kDirectSeqs sequences) what a CTA needs to find
+// its piece by itself.
 struct DecayLists {
   int* counts;
   Piece* pieces;
   Split* splits;
   float* states;
+  const int32_t* off;
+  int n_seq, total;
+  DecayCut cut;
 };
 
 // What a plan makes: the list of query tiles and, for a backward, of key tiles.
@@ -178,9 +183,7 @@ struct DecayCall {
   DecayRun r[kMaxRuns];
   int runs, sets;  // sets of piece states
 };
-cudaError_t launch_decay_plan(const DecayProblem& p, const DecayCut& cut, const int32_t* off,
-                              const float* log_decay, const DecayLists& l, int* err,
-                              cudaStream_t s);
+cudaError_t launch_decay_plan(const DecayLists& l, int* err, cudaStream_t s);
 // The states before each piece of the cut sequences, into their slots: every
 // piece's own sum, then a walk over the pieces.  Then the runs themselves.
 cudaError_t launch_decay_pieces(const DecayProblem& p, const DecayCut& cut, const DecayCall& c,
@@ -218,7 +221,7 @@ __device__ __forceinline__ Seq checked_seq(const SeqIn& in, int i, bool* good) {
   return *good ? Seq{int(q0), int(q1 - q0), int(k0), int(k1 - k0)} : Seq{0, 0, 0, 0};
 }
 
-// The warp's number, and one elected lane, in a form that the compiler knows to be the same
+// The warp's number, a value, and one elected lane, in a form that the compiler knows to be the same
 // for the whole warp.  Products and TMA copies take their operands from uniform registers;
 // issued from a branch on threadIdx they cost about 150 cycles each, whatever their size,
 // issued by an elected lane of a converged warp 48 (N = 64), 64 (N = 128), the tensor pipe's
@@ -226,6 +229,7 @@ __device__ __forceinline__ Seq checked_seq(const SeqIn& in, int i, bool* good) {
 __device__ __forceinline__ int uniform_warp() {
   return __shfl_sync(0xffffffffu, int(threadIdx.x) / 32, 0);
 }
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ bool elect_sync() {
   uint32_t p;
   asm volatile(
@@ -236,20 +240,190 @@ __device__ __forceinline__ bool elect_sync() {
   return p != 0;
 }
 
-// Item `idx` of a list of query tiles (or key tiles); false if there are fewer.
-__device__ __forceinline__ bool fetch_item(const ItemList& l, int idx, bool keys, Item* it,
-                                           int* err) {
+// Keys that query tile t sees, or queries that see key tile t, in 128s.
+__device__ __forceinline__ int item_cost(const Seq& s, int t, int tile, bool keys) {
+  const long long off = (long long)s.nk - s.nq;
+  if (keys) {
+    const long long first = max(0ll, (long long)t * tile - off);
+    return first < s.nq ? int((s.nq - first + 127) >> 7) : 0;
+  }
+  const long long last = min((long long)s.nq, (long long)(t + 1) * tile) + off;
+  return last > 0 ? int((last + 127) >> 7) : 0;
+}
+// How many of a sequence's n tiles cost at least c: the last ones of the query tiles, the
+// first ones of the key tiles.  A tile has a power of two rows.
+__device__ __forceinline__ int items_from(const Seq& s, int n, int tile, bool keys, int c) {
+  if (n == 0 || c <= 0) return n;
+  const int bits = __ffs(tile) - 1;
+  const long long off = (long long)s.nk - s.nq;
+  if (keys) {
+    const long long left = s.nq - (c - 1) * 128ll, to = left + off;  // t * tile < to
+    return left <= 0 || to <= 0 ? 0 : int(min((long long)n, (to + tile - 1) >> bits));
+  }
+  if (item_cost(s, n - 1, tile, false) < c) return 0;
+  const long long from = (c - 1) * 128ll - off;  // (t + 1) * tile > from
+  return n - (from > 0 ? int(from >> bits) : 0);
+}
+
+// Item `idx` of a list of query tiles (or key tiles); false if there are fewer.  A whole warp.
+// Without a list: a lane holds a sequence; the cost of the item is found by bisection on the
+// number of tiles that cost at least so much (about 1 us against 7 us for making the list).
+__device__ __forceinline__ bool find_item(const ItemList& l, int idx, bool keys, Item* it,
+                                          int* err) {
+  constexpr uint32_t kAll = 0xffffffffu;
   if (l.items) {
     if (idx >= *l.count) return false;
     *it = l.items[idx];
     return true;
   }
-  bool good;
-  const Seq s = checked_seq(l.in, 0, &good);
-  if (!good && threadIdx.x == 0) set_error(err, SLA_ERR_DEVICE);
+  const int lane = lane_id();
+  Seq s{0, 0, 0, 0};
+  if (lane < l.in.n_seq) {
+    bool good;
+    s = checked_seq(l.in, lane, &good);
+    if (!good) set_error(err, SLA_ERR_DEVICE);
+  }
   const int n = ((keys ? s.nk : s.nq) + l.tile - 1) / l.tile;
-  if (idx >= n) return false;
-  *it = Item{s, keys ? idx : n - 1 - idx, 0, 0, 0};
+  const int all = int(__reduce_add_sync(kAll, unsigned(n)));
+  if (all > l.most) set_error(err, SLA_ERR_DEVICE);  // sequences that overlap: some are left out
+  if (idx >= all) return false;
+  const auto from = [&](int c) {
+    return int(__reduce_add_sync(kAll, unsigned(items_from(s, n, l.tile, keys, c))));
+  };
+  // the largest c with more than idx tiles of at least c
+  int lo = 0, hi = n ? item_cost(s, keys ? 0 : n - 1, l.tile, keys) : 0;
+  hi = __reduce_max_sync(kAll, unsigned(hi)) + 1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (from(mid) > idx)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int least = items_from(s, n, l.tile, keys, lo), above = items_from(s, n, l.tile, keys, hi);
+  const int mine = least - above;
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kAll, before, o);
+    if (lane >= o) before += x;
+  }
+  before -= mine;
+  const int k = idx - from(hi) - before;
+  const int who = __ffs(__ballot_sync(kAll, k >= 0 && k < mine)) - 1;
+  const int t = keys ? above + k : n - least + k;
+  const auto pick = [&](int x) { return __shfl_sync(kAll, x, who); };
+  *it = Item{Seq{pick(s.q0), pick(s.nq), pick(s.k0), pick(s.nk)}, pick(t), who, 0, 0};
+  return true;
+}
+
+// The CTA's item, found by its first warp and handed to the others through `place` (shared).
+struct ItemPlace {
+  Item it;
+  int found;
+};
+__device__ __forceinline__ bool fetch_item(const ItemList& l, int idx, bool keys, Item* it,
+                                           ItemPlace* place, int* err) {
+  if (uniform_warp() == 0) {
+    Item x{};
+    const bool found = find_item(l, idx, keys, &x, err);
+    if (lane_id() == 0) *place = ItemPlace{x, found};
+  }
+  __syncthreads();
+  const Item& x = place->it;
+  *it = Item{Seq{uniform(x.s.q0), uniform(x.s.nq), uniform(x.s.k0), uniform(x.s.nk)},
+             uniform(x.tile), uniform(x.seq), 0, 0};
+  return uniform(place->found) != 0;
+}
+
+// Pieces of the lane's sequence: 0 for none or a bad one (reported), else how many.
+__device__ __forceinline__ int own_pieces(const DecayLists& l, int lane, int* row, int* rows,
+                                          int* err) {
+  *row = *rows = 0;
+  if (lane >= l.n_seq) return 0;
+  const int a = l.off[lane], b = l.off[lane + 1];
+  if (a < 0 || b < a || b > l.total) {
+    if (err) set_error(err, SLA_ERR_DEVICE);
+    return 0;
+  }
+  *row = a;
+  *rows = b - a;
+  const int n = (b - a + l.cut.rows - 1) / l.cut.rows;
+  return n > 1 ? n : 1;
+}
+__device__ __forceinline__ int lanes_before(int x) {  // sum over the lanes before this one
+  int sum = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (int(lane_id()) >= o) sum += y;
+  }
+  return sum - x;
+}
+// The idx-th piece, those of cut sequences first (idx is their slot); false if there are fewer.
+// A whole warp.
+__device__ __forceinline__ bool find_piece(const DecayLists& l, int idx, Piece* pc, int* err) {
+  const int slots = l.cut.most_slots;
+  if (l.pieces) {
+    const int cut = l.counts[0];
+    if (idx >= cut + l.counts[2]) return false;
+    *pc = l.pieces[idx < cut ? idx : slots + idx - cut];
+    return true;
+  }
+  constexpr uint32_t kAll = 0xffffffffu;
+  int row, rows;
+  const int n = own_pieces(l, lane_id(), &row, &rows, err);
+  int cut = n > 1 ? n : 0;
+  const int at = lanes_before(cut), rank = lanes_before(n == 1);
+  if (cut > 0 && at + cut > slots) {  // sequences that overlap: some are left out
+    set_error(err, SLA_ERR_DEVICE);
+    cut = 0;
+  }
+  const int cuts = int(__reduce_add_sync(kAll, unsigned(cut)));
+  const int k = idx < cuts ? idx - at : idx - cuts - rank;
+  const bool mine = idx < cuts ? k >= 0 && k < cut : n == 1 && k == 0;
+  const int who = __ffs(__ballot_sync(kAll, mine)) - 1;
+  if (who < 0) return false;
+  const auto pick = [&](int x) { return __shfl_sync(kAll, x, who); };
+  const int j = idx < cuts ? pick(k) : 0;
+  const int r0 = pick(row), all = pick(rows), pieces = pick(n);
+  *pc = Piece{r0 + j * l.cut.rows, min(l.cut.rows, all - j * l.cut.rows), who,
+              idx < cuts ? idx : -1, j == 0, j == pieces - 1, 0, 0};
+  return true;
+}
+struct PiecePlace {
+  Piece pc;
+  int found;
+};
+__device__ __forceinline__ bool fetch_piece(const DecayLists& l, int idx, Piece* pc,
+                                            PiecePlace* place, int* err) {
+  if (uniform_warp() == 0) {
+    Piece x{};
+    const bool found = find_piece(l, idx, &x, err);
+    if (lane_id() == 0) *place = PiecePlace{x, found};
+  }
+  __syncthreads();
+  const Piece& x = place->pc;
+  *pc = Piece{uniform(x.row),   uniform(x.rows), uniform(x.seq), uniform(x.slot),
+              uniform(x.first), uniform(x.last), 0,              0};
+  return uniform(place->found) != 0;
+}
+// The idx-th cut sequence; false if there are fewer.  A whole warp.
+__device__ __forceinline__ bool fetch_split(const DecayLists& l, int idx, Split* sp) {
+  if (l.pieces) {
+    if (idx >= l.counts[1]) return false;
+    *sp = l.splits[idx];
+    return true;
+  }
+  int row, rows;
+  const int n = own_pieces(l, lane_id(), &row, &rows, nullptr);
+  const int cut = n > 1 ? n : 0, at = lanes_before(cut);
+  const bool fits = cut > 0 && at + cut <= l.cut.most_slots;
+  const int rank = lanes_before(fits);
+  const int who = __ffs(__ballot_sync(0xffffffffu, fits && rank == idx)) - 1;
+  if (who < 0) return false;
+  const auto pick = [&](int x) { return __shfl_sync(0xffffffffu, x, who); };
+  *sp = Split{who, pick(at), pick(n), pick(rows - (n - 1) * l.cut.rows)};
   return true;
 }
 

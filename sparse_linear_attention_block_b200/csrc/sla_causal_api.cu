@@ -140,9 +140,9 @@ DecayCut decay_cut(const DecayProblem& p, int runs) {
   DecayCut c{};
   c.rows = int(rows < 256 ? 256 : rows > kMaxRows ? kMaxRows : rows);
   if (p.total > c.rows) {
-    // a cut sequence has n >= 2 pieces and more than (n - 1) rows of them
-    c.most_slots = int(2ll * p.total / c.rows);
-    c.most_splits = p.total / c.rows;
+    // a cut sequence has more than one piece's rows, and one piece that may not be whole
+    c.most_splits = p.total / c.rows < p.n_seq ? p.total / c.rows : p.n_seq;
+    c.most_slots = p.total / c.rows + c.most_splits;
   }
   return c;
 }
@@ -159,10 +159,18 @@ DecayLayout decay_layout(const DecayProblem& p, const DecayCut& c) {
   return L;
 }
 
-DecayLists decay_lists(void* ws, const DecayLayout& L) {
+DecayLists decay_lists(void* ws, const DecayLayout& L, const DecayProblem& p, const DecayCut& cut,
+                       const int32_t* off) {
   uint8_t* b = static_cast<uint8_t*>(ws);
-  return {reinterpret_cast<int*>(b + L.counts), reinterpret_cast<Piece*>(b + L.pieces),
-          reinterpret_cast<Split*>(b + L.splits), reinterpret_cast<float*>(b + L.states)};
+  const bool direct = p.n_seq <= kDirectSeqs;
+  return {reinterpret_cast<int*>(b + L.counts),
+          direct ? nullptr : reinterpret_cast<Piece*>(b + L.pieces),
+          reinterpret_cast<Split*>(b + L.splits),
+          reinterpret_cast<float*>(b + L.states),
+          off,
+          p.n_seq,
+          p.total,
+          cut};
 }
 
 sla_status check_workspace(const void* ws, size_t bytes, size_t need) {
@@ -248,7 +256,7 @@ sla_status sla_causal_forward(const sla_causal_shape* shape, const void* q, cons
     return SLA_OK;
   }
   int* counts = at<int>(workspace, L.counts);
-  Item* items = p.n_seq > 1 ? at<Item>(workspace, L.items) : nullptr;
+  Item* items = p.n_seq > kDirectSeqs ? at<Item>(workspace, L.items) : nullptr;
   const int most = int(most_items(p.total_q, fwd_tile(p), p.n_seq));
   if (items) {
     const CausalPlan plan{fwd_tile(p), most, items, counts, 0, nullptr, nullptr};
@@ -280,7 +288,7 @@ sla_status sla_causal_backward(const sla_causal_shape* shape, const void* q, con
   float* dvec = at<float>(workspace, L.dvec);
   const int most = int(most_items(p.total_q, fwd_tile(p), p.n_seq)),
             kmost = int(most_items(p.total_k, kRowTile, p.n_seq));
-  if (p.n_seq > 1) {
+  if (p.n_seq > kDirectSeqs) {
     items = at<Item>(workspace, L.items);
     kitems = at<Item>(workspace, L.kitems);
     const CausalPlan plan{fwd_tile(p), most, items, counts, kmost, kitems, counts + 1};
@@ -322,8 +330,8 @@ sla_status sla_decay_forward(const sla_decay_shape* shape, const void* q, const 
   if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = at<int>(workspace, L.err);
-  const DecayLists l = decay_lists(workspace, L);
-  SLA_LAUNCH("decay_plan", s, launch_decay_plan(p, cut, off, log_decay, l, err, s));
+  const DecayLists l = decay_lists(workspace, L, p, cut, off);
+  if (l.pieces) SLA_LAUNCH("decay_plan", s, launch_decay_plan(l, err, s));
   DecayCall c{};
   c.t[0] = view(q, p.q);
   c.t[1] = view(k, p.k);
@@ -351,8 +359,8 @@ sla_status sla_decay_backward(const sla_decay_shape* shape, const void* q, const
   if ((st = check_workspace(workspace, workspace_bytes, L.total)) != SLA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = at<int>(workspace, L.err);
-  const DecayLists l = decay_lists(workspace, L);
-  SLA_LAUNCH("decay_plan", s, launch_decay_plan(p, cut, off, log_decay, l, err, s));
+  const DecayLists l = decay_lists(workspace, L, p, cut, off);
+  if (l.pieces) SLA_LAUNCH("decay_plan", s, launch_decay_plan(l, err, s));
   DecayCall c{};
   c.t[0] = view(q, p.q);
   c.t[1] = view(k, p.k);

@@ -102,6 +102,7 @@ struct DqBars {
   static constexpr int kSt = DqSmem<D>::kSt;
   uint64_t q_full, k_full[kSt], k_empty[kSt], v_full[kSt], v_empty[kSt], k_fix, s_full[2],
       ds_full[2], o_full[2], mma_done;
+  ItemPlace place;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -117,8 +118,6 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
   constexpr int kSt = L::kSt;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int item = blockIdx.x / g.heads, hx = blockIdx.x % g.heads;
-  Item it;
-  if (!fetch_item(g.list, item, false, &it, g.err)) return;
   if ((smem_u32(smem_raw) & 1023u) != 0u) {
     if (threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
     return;
@@ -128,6 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
   uint8_t* sK = sDO + 2 * L::kQ;
   uint8_t* sV = sK + kSt * L::kKV;
   DqBars<D>& bb = *reinterpret_cast<DqBars<D>*>(smem_raw + L::kTiles);
+  Item it;
+  if (!fetch_item(g.list, item, false, &it, &bb.place, g.err)) return;
   int* err = g.err;
   volatile int* abort_flag = &bb.abort_flag;
   const int warp = uniform_warp(), lane = lane_id();
@@ -364,6 +365,7 @@ struct DkBars {
   using L = DkSmem<D>;
   uint64_t kv_full, q_full[L::kQSt], q_empty[L::kQSt], o_full[L::kOSt], o_empty[L::kOSt],
       l_full[L::kLSt], l_empty[L::kLSt], q_fix, o_fix, s_full, p_full, dp_full, ds_full, acc_full, mma_done;
+  ItemPlace place;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -378,8 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
   using L = DkSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const int item = blockIdx.x / g.heads, hk = blockIdx.x % g.heads;
-  Item it;
-  if (!fetch_item(g.list, item, true, &it, g.err)) return;
   if ((smem_u32(smem_raw) & 1023u) != 0u) {
     if (threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
     return;
@@ -390,6 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
   uint8_t* sDO = sQ + L::kQSt * L::kT;
   float* sLd = reinterpret_cast<float*>(smem_raw + L::kTiles);
   DkBars<D>& bb = *reinterpret_cast<DkBars<D>*>(smem_raw + L::kTiles + L::kLd);
+  Item it;
+  if (!fetch_item(g.list, item, true, &it, &bb.place, g.err)) return;
   int* err = g.err;
   volatile int* abort_flag = &bb.abort_flag;
   const int warp = uniform_warp(), lane = lane_id();

@@ -8,17 +8,6 @@ namespace {
 
 constexpr int kPlanThreads = 1024, kBuckets = 2048;
 
-// Keys that query tile t sees, or queries that see key tile t, in 128s.
-__device__ __forceinline__ int item_cost(const Seq& s, int t, int tile, bool keys) {
-  const long long off = (long long)s.nk - s.nq;
-  if (keys) {
-    const long long first = max(0ll, (long long)t * tile - off);
-    return first < s.nq ? int((s.nq - first + 127) / 128) : 0;
-  }
-  const long long last = min((long long)s.nq, (long long)(t + 1) * tile) + off;
-  return last > 0 ? int((last + 127) / 128) : 0;
-}
-
 // One CTA per list: the tiles of all sequences by a counting sort on their
 // cost, the most expensive first, so that the long tiles of a causal mask do
 // not start last.  The order among equals is left open: no result depends on
@@ -89,13 +78,13 @@ __global__ void __launch_bounds__(kPlanThreads) causal_plan_kernel(SeqIn in, int
 // places in the lists are handed out by counters in shared memory; no result
 // depends on them.
 __global__ void __launch_bounds__(kPlanThreads) decay_plan_kernel(
-    const int32_t* __restrict__ off, const float* __restrict__ log_decay, int n_seq, int total,
-    int H, DecayCut cut, DecayLists l, int* err) {
+    DecayLists l, int* err) {
+  const int32_t* __restrict__ off = l.off;
+  const int n_seq = l.n_seq, total = l.total;
+  const DecayCut cut = l.cut;
   __shared__ int slots, splits, whole, end;
   if (threadIdx.x == 0) slots = splits = whole = end = 0;
   __syncthreads();
-  for (int h = threadIdx.x; h < H; h += kPlanThreads)
-    if (!(log_decay[h] <= 0.f)) set_error(err, SLA_ERR_DEVICE);
   const int lane = threadIdx.x % 32;
   for (int i = threadIdx.x / 32; i < n_seq; i += kPlanThreads / 32) {
     const int a = off[i], b = off[i + 1];
@@ -147,10 +136,8 @@ cudaError_t launch_causal_plan(const SeqIn& in, const CausalPlan& plan, int* err
   return cudaGetLastError();
 }
 
-cudaError_t launch_decay_plan(const DecayProblem& p, const DecayCut& cut, const int32_t* off,
-                              const float* log_decay, const DecayLists& l, int* err,
-                              cudaStream_t s) {
-  decay_plan_kernel<<<1, kPlanThreads, 0, s>>>(off, log_decay, p.n_seq, p.total, p.H, cut, l, err);
+cudaError_t launch_decay_plan(const DecayLists& l, int* err, cudaStream_t s) {
+  decay_plan_kernel<<<1, kPlanThreads, 0, s>>>(l, err);
   return cudaGetLastError();
 }
 

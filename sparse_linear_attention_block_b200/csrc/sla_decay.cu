@@ -64,26 +64,25 @@ struct DrSmem {
   static constexpr int kPlaces = 4, kPair = 2 * kT;
   static_assert(kPlaces * kPair + 6 * kT <= kPow, "y, z and the parts of w y");
   // one CTA per SM, as it takes all of TMEM
-  static constexpr int kTotal = kBars + 256 > 116 * 1024 ? kBars + 256 : 116 * 1024;
+  static constexpr int kTotal = kBars + 320 > 116 * 1024 ? kBars + 320 : 116 * 1024;
   static_assert(kTotal <= 227 * 1024, "shared memory of a CTA");
 };
 struct DrBars {
   Factor carry[2];  // of a whole chunk, of the piece's last one
   uint64_t in_full[4], split_full[2], a_full[2], p_full[2], u_full[2], o_full[2], u_free, s_full,
       o1_done, o_free, fin;
+  PiecePlace place;
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(DrBars) <= 256, "the place of the barriers");
+static_assert(sizeof(DrBars) <= 320, "the place of the barriers");
 
 struct DrArgs {
   CUtensorMap tm[kMaxTensors], tm_out[kMaxRuns];
-  const int* counts;
-  const Piece* pieces;
-  float* states;
+  DecayLists l;
   const float* log_decay;
   DecayRun r[kMaxRuns];
-  int H, most_slots;
+  int H;
   float scale;
   int* err;
 };
@@ -103,15 +102,6 @@ __global__ void __launch_bounds__(kRunThreads, 1)
   using L = DrSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int idx = blockIdx.x / g.H, h = blockIdx.x % g.H;
-  if (kStateOnly ? idx >= g.counts[0]
-                 : !(idx < g.counts[0] ||
-                     (idx >= g.most_slots && idx - g.most_slots < g.counts[2])))
-    return;
-  const Piece pc = g.pieces[idx];
-  const DecayRun& run = g.r[blockIdx.y];
-  const bool rev = run.reverse;
-  // the walk over the pieces does not need the last one's sum
-  if (kStateOnly && (!run.makes || (rev ? pc.first : pc.last))) return;
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (threadIdx.x == 0) set_error(g.err, SLA_ERR_DEVICE);
     return;
@@ -119,11 +109,18 @@ __global__ void __launch_bounds__(kRunThreads, 1)
   float* pw = reinterpret_cast<float*>(smem + L::kPow);
   float* mix = reinterpret_cast<float*>(smem + L::kMix);
   DrBars& bb = *reinterpret_cast<DrBars*>(smem + L::kBars);
+  Piece pc;
+  if (!fetch_piece(g.l, idx, &pc, &bb.place, g.err)) return;
+  const DecayRun& run = g.r[blockIdx.y];
+  const bool rev = run.reverse;
+  // whole sequences need no sum, and the walk over the pieces not the last one's
+  if (kStateOnly && (!run.makes || pc.slot < 0 || (rev ? pc.first : pc.last))) return;
   int* err = g.err;
   volatile int* abort_flag = &bb.abort_flag;
   const int t = threadIdx.x, warp = uniform_warp(), lane = t % 32;
   const int tl = t & 127;  // thread of a warpgroup: TMEM lane
   const float gl = decay_checked(g.log_decay[h]);
+  if (threadIdx.x == 0 && !(g.log_decay[h] <= 0.f)) set_error(g.err, SLA_ERR_DEVICE);
   const int chunks = (pc.rows + 63) / 64, tail = pc.rows - (chunks - 1) * 64;
 
   if (warp == 0) tmem_alloc(&bb.tmem_base, 512);
@@ -194,7 +191,7 @@ __global__ void __launch_bounds__(kRunThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  float* const slots = g.states + size_t(run.slots) * g.most_slots * g.H * D * D;
+  float* const slots = g.l.states + size_t(run.slots) * g.l.cut.most_slots * g.H * D * D;
   bool ok = true;
 
   if (warp < 4) {
@@ -535,24 +532,22 @@ __global__ void __launch_bounds__(kRunThreads, 1)
 // the j-th piece's sum and n_j its rows,  S_0 = state_in,  S_{j+1} = l^{n_j} S_j + U_j.
 // Four elements per thread.
 struct DsArgs {
-  const int* counts;
-  const Split* splits;
-  float* states;
+  DecayLists l;
   const float* log_decay;
   DecayRun r[2];  // the run that makes each set
-  int H, rows, most_slots;
+  int H;
 };
 template <int D>
 __global__ void __launch_bounds__(256) decay_scan_kernel(const __grid_constant__ DsArgs g) {
   constexpr int kParts = D * D / 1024;
-  if (int(blockIdx.x) >= g.counts[1]) return;
-  const Split sp = g.splits[blockIdx.x];
+  Split sp;
+  if (!fetch_split(g.l, blockIdx.x, &sp)) return;
   const int h = blockIdx.y, H = g.H, set = blockIdx.z / kParts;
   const int e = (blockIdx.z % kParts * 256 + threadIdx.x) * 4;
   const DecayRun& r = g.r[set];
-  float* const states = g.states + size_t(set) * g.most_slots * H * D * D;
+  float* const states = g.l.states + size_t(set) * g.l.cut.most_slots * H * D * D;
   const float gl = decay_checked(g.log_decay[h]);
-  const Factor full = decay_factor(gl, g.rows), part = decay_factor(gl, sp.last_rows);
+  const Factor full = decay_factor(gl, g.l.cut.rows), part = decay_factor(gl, sp.last_rows);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (r.state_in) {
     const float* p = r.state_in + (size_t(sp.seq) * H + h) * D * D;
@@ -648,20 +643,17 @@ cudaError_t run(const DecayProblem& p, const DecayCut& cut, const DecayCall& c, 
     if (!make_tmap_rows(&a.tm_out[i], o.p, p.total, p.H, D, sla_strides{o.row, o.head}, 64))
       return cudaErrorInvalidValue;
   }
-  a.counts = l.counts;
-  a.pieces = l.pieces;
-  a.states = l.states;
+  a.l = l;
   a.log_decay = log_decay;
   for (int i = 0; i < c.runs; ++i) a.r[i] = c.r[i];
   a.H = p.H;
-  a.most_slots = cut.most_slots;
   a.scale = p.scale;
   a.err = err;
   auto* kernel = decay_run_kernel<D, kStateOnly>;
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DrSmem<D>::kTotal);
   if (e != cudaSuccess) return e;
-  const dim3 grid(unsigned(cut.most_slots + (kStateOnly ? 0 : p.n_seq)) * p.H,
+  const dim3 grid(unsigned(kStateOnly ? cut.most_slots : p.total / cut.rows + p.n_seq) * p.H,
                   kStateOnly ? c.sets : c.runs);  // the runs that make a set come first
   kernel<<<grid, kRunThreads, DrSmem<D>::kTotal, s>>>(a);
   return cudaGetLastError();
@@ -685,8 +677,7 @@ cudaError_t launch_decay_pieces(const DecayProblem& p, const DecayCut& cut, cons
 
 cudaError_t launch_decay_scan(const DecayProblem& p, const DecayCut& cut, const DecayCall& c,
                               const DecayLists& l, const float* log_decay, cudaStream_t s) {
-  DsArgs a{l.counts, l.splits, l.states, log_decay, {c.r[0], c.r[1]}, p.H, cut.rows,
-           cut.most_slots};
+  const DsArgs a{l, log_decay, {c.r[0], c.r[1]}, p.H};
   const dim3 grid(cut.most_splits, p.H, p.d * p.d / 1024 * c.sets);
   if (p.d == 128)
     decay_scan_kernel<128><<<grid, 256, 0, s>>>(a);

@@ -218,6 +218,17 @@ def test_rising_scores():
     c.check()
 
 
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 200])
+def test_many_sequences(n):
+    """A CTA finds its tile by itself among up to 32 sequences, from a list beyond."""
+    lq = [(i * 37) % 150 for i in range(n)]
+    lk = [a + (i * 11) % 90 for i, a in enumerate(lq)]
+    c = Case(lq, lk, Hq=2, Hkv=1, d=64, seed=n, lead=2, tail=3, backward=True)
+    c.forward()
+    c.backward()
+    c.check(backward=True)
+
+
 def test_own_scale_and_max_q():
     c = Case([77, 130], Hq=2, Hkv=2, d=128, scale=0.03, max_q=130, seed=6)
     c.forward()
@@ -245,6 +256,22 @@ def test_bad_offsets_are_skipped_and_reported():
     assert (c.buf.o[:60] == 77.0).all()
     c.seqs = c.seqs[1:]
     c.check()
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_offsets_that_fall_back_stay_in_bounds(n):
+    """Every second sequence falls back to row 0, so the rest overlap and ask for more tiles than
+    there are rows: what is written is written within the tensors, and it is reported."""
+    c = Case([400] + [0] * (n - 1), Hq=2, Hkv=1, d=64, seed=8, tail=8, backward=True)
+    bad = [0 if i % 2 == 0 else 400 for i in range(n + 1)]
+    c.q_off.copy_(i32(bad))
+    c.k_off.copy_(i32(bad))
+    c.forward()
+    c.backward()
+    with pytest.raises(slab.SlaError) as e:
+        slab.sla_check(c.buf.workspace)
+    assert e.value.status == 6
+    assert (c.buf.o[400:] == 77.0).all() and (c.buf.dk[400:] == 77.0).all()
 
 
 def test_equal_inputs_give_equal_bits():

@@ -117,6 +117,32 @@ def test_long_prompts_of_few_heads():
     ref.check("d_state", b.d_state, r["d_state"], 4 * t["d_state"], 2.0 ** -17)
 
 
+@pytest.mark.parametrize("n", [1, 32, 33, 150])
+def test_many_sequences(n):
+    """A CTA finds its piece by itself among up to 32 sequences, from a list beyond; some of the
+    sequences are cut."""
+    lengths = [(i * 53) % 90 for i in range(n)]
+    lengths[n // 2] = 1300
+    lengths[-1] = 700
+    c = Case(lengths, H=2, d=64, seed=n, log_decay=[-0.003, -0.2], lead=1, tail=2, backward=True)
+    c.forward()
+    c.backward()
+    c.check(backward=True)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_offsets_that_fall_back_stay_in_bounds(n):
+    c = Case([1500] + [0] * (n - 1), H=2, d=64, seed=8, tail=8, log_decay=[-0.1, -0.2],
+             backward=True)
+    c.off.copy_(i32([0 if i % 2 == 0 else 1500 for i in range(n + 1)]))
+    c.forward()
+    c.backward()
+    with pytest.raises(slab.SlaError) as e:
+        slab.sla_check(c.buf.workspace)
+    assert e.value.status == 6
+    assert (c.buf.o[1500:] == 77.0).all() and (c.buf.dk[1500:] == 77.0).all()
+
+
 def test_state_in_place_and_in_two_parts():
     """A prompt in two calls through one state buffer gives what one call gives."""
     c = Case([400, 90], H=2, d=64, seed=9, log_decay=[-0.01, -0.3])

@@ -140,11 +140,11 @@ cudaError_t launch_causal_token(const CausalProblem& p, const void* q, const voi
 cudaError_t launch_causal_dvec(const CausalProblem& p, const void* o, const void* d_o, float* dvec,
                                cudaStream_t s);
 cudaError_t launch_causal_dq(const CausalProblem& p, const void* q, const void* k, const void* v,
-                             const ItemList& list, const void* d_o, const float* lse,
-                             const float* dvec, void* dq, int* err, cudaStream_t s);
+                             const ItemList& list, const void* d_o, const float* lse, float* dvec,
+                             void* dq, int* err, cudaStream_t s);
 cudaError_t launch_causal_dkv(const CausalProblem& p, const void* q, const void* k, const void* v,
-                              const ItemList& list, const void* d_o, const float* lse,
-                              const float* dvec, void* dk, void* dv, int* err, cudaStream_t s);
+                              const ItemList& list, const void* d_o, const float* lse, float* dvec,
+                              void* dk, void* dv, int* err, cudaStream_t s);
 
 // TMA descriptor of a bf16 [rows, heads, d] tensor with the given strides: coordinates
 // (feature, row, head), boxes of 64 features x box_rows rows of one head, 128-byte swizzle.

@@ -297,9 +297,10 @@ sla_status sla_causal_backward(const sla_causal_shape* shape, const void* q, con
   const ItemList list{counts, items, most, in, fwd_tile(p)};
   const ItemList klist{counts + 1, kitems, kmost, in, kRowTile};
   SLA_LAUNCH("causal_dvec", s, launch_causal_dvec(p, o, d_o, dvec, s));
+  // dQ first: it leaves D without the error that o's rounding gives it
+  SLA_LAUNCH("causal_dq", s, launch_causal_dq(p, q, k, v, list, d_o, lse, dvec, dq, err, s));
   SLA_LAUNCH("causal_dkv", s,
              launch_causal_dkv(p, q, k, v, klist, d_o, lse, dvec, dk, dv, err, s));
-  SLA_LAUNCH("causal_dq", s, launch_causal_dq(p, q, k, v, list, d_o, lse, dvec, dq, err, s));
   return SLA_OK;
 }
 

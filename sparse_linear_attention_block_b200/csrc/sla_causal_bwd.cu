@@ -20,7 +20,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct CbArgs {
   ItemList list;
-  const float *lse, *dvec;
+  const float* lse;
+  float* dvec;
   RowOut out0, out1;  // dq; or dk and dv
   int total_q, heads, G, pair_heads;
   float scale, scale_log2;
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
     mbar_init(&bb.k_fix, 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&bb.s_full[h], 1);
-      mbar_init(&bb.ds_full[h], 128);
+      mbar_init(&bb.ds_full[h], 4);
       mbar_init(&bb.o_full[h], 1);
     }
     mbar_init(&bb.mma_done, 1);
@@ -257,9 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
         const uint64_t kd = desc_mnmajor_base(smem_u32(sK + (j % kSt) * L::kKV), 64);
         if (elect_sync()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
+          for (int ks = 0; ks < 8; ++ks)  // the high parts, then the low ones
             mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
-                   desc_advance(kd, mnmajor_step_bytes(ks)), id_q, (j | ks) != 0);
+                   desc_advance(kd, mnmajor_step_bytes(ks & 3)), id_q, (j | ks) != 0);
           if (j == n[h] - 1) mma_commit(&bb.o_full[h]);
         }
         __syncwarp();
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
     const float dd = real ? g.dvec[size_t(hd) * g.total_q + row] : 0.f;
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + h * 128, to = tmem + lane_base + 256 + h * 128;
+    float2 slip = make_float2(0.f, 0.f);
     bool ok = true;
     for (int j = 0; j < nh; ++j) {
       ok = mbar_wait(&bb.s_full[h], j & 1, err, abort_flag);
@@ -309,29 +311,48 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
         tmem_ld32(ts + 64 + c * 32, reinterpret_cast<float(&)[32]>(pv[c * 32]));
       }
       tmem_ld_wait();
+      const float2 f2 = make_float2(g.scale_log2, g.scale_log2), b2 = make_float2(-base, -base),
+                   d2 = make_float2(-dd, -dd);
 #pragma unroll
-      for (int e = 0; e < 64; ++e)
-        sv[e] = exp2f(fmaf(sv[e], g.scale_log2, -base)) * (pv[e] - dd);
+      for (int e = 0; e < 64; e += 2) {
+        const float2 x = __ffma2_rn(make_float2(sv[e], sv[e + 1]), f2, b2);
+        const float2 y = __fmul2_rn(make_float2(exp2f(x.x), exp2f(x.y)),
+                                    __fadd2_rn(make_float2(pv[e], pv[e + 1]), d2));
+        sv[e] = y.x;
+        sv[e + 1] = y.y;
+      }
       if ((j + 1) * 64 > lim0) {
         const int left = lim - j * 64;
 #pragma unroll
         for (int e = 0; e < 64; ++e) sv[e] = e < left ? sv[e] : 0.f;
       }
+      // dS as two bf16 numbers, the second 32 columns further
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t pk[8];
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) pk[e] = pack_bf16(sv[c * 16 + 2 * e], sv[c * 16 + 2 * e + 1]);
-        tmem_st8(ts + c * 8, pk);
+        for (int e = 0; e < 8; ++e) {
+          const float2 x = make_float2(sv[c * 16 + 2 * e], sv[c * 16 + 2 * e + 1]);
+          hi[e] = pack_bf16(x.x, x.y);
+          const float2 r = __ffma2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])),
+                                      make_float2(-1.f, -1.f), x);
+          lo[e] = pack_bf16(r.x, r.y);
+          slip = __fadd2_rn(slip, x);
+        }
+        tmem_st8(ts + c * 8, hi);
+        tmem_st8(ts + 32 + c * 8, lo);
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&bb.ds_full[h]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bb.ds_full[h]);
     }
     if (ok && nh > 0) {
       ok = mbar_wait(&bb.o_full[h], 0, err, abort_flag);
       tc_fence_after();
     }
+    // sum_b dS_ab = D_a - (the D used), as the weights add up to 1: the dK kernel gets it right
+    if (ok && real) g.dvec[size_t(hd) * g.total_q + row] = dd + (slip.x + slip.y);
     __nv_bfloat16* dst = g.out0.p + row * g.out0.row + hd * g.out0.head;
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32) store_row32(to + c0, ok && nh > 0, real, g.scale, dst + c0);
@@ -358,7 +379,7 @@ struct DkSmem {
   static constexpr int kT = 128 * D * 2;
   static constexpr int kQSt = 3, kOSt = 2, kLSt = 2;
   static constexpr int kTiles = (2 + kQSt + kOSt) * kT;  // K, V, Q ring, dO ring
-  static constexpr int kLd = kLSt * 2 * 128 * 4;         // lse log2(e), then D, per stage
+  static constexpr int kLd = kLSt * 2 * 128 * 4;         // -lse log2(e), then -D, per stage
 };
 template <int D>
 struct DkBars {
@@ -420,9 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
     mbar_init(&bb.q_fix, 1);
     mbar_init(&bb.o_fix, 1);
     mbar_init(&bb.s_full, 1);
-    mbar_init(&bb.p_full, 256);
+    mbar_init(&bb.p_full, 8);
     mbar_init(&bb.dp_full, 1);
-    mbar_init(&bb.ds_full, 256);
+    mbar_init(&bb.ds_full, 8);
     mbar_init(&bb.acc_full, 1);
     mbar_init(&bb.mma_done, 1);
     bb.abort_flag = 0;
@@ -573,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int x = a + e * 32 + lane;
-          dst[e * 32 + lane] = x < it.s.nq ? g.lse[at + x] * kLog2e : 0.f;
-          dst[128 + e * 32 + lane] = x < it.s.nq ? g.dvec[at + x] : 0.f;
+          dst[e * 32 + lane] = x < it.s.nq ? -g.lse[at + x] * kLog2e : 0.f;
+          dst[128 + e * 32 + lane] = x < it.s.nq ? -g.dvec[at + x] : 0.f;
         }
         mbar_arrive(&bb.l_full[i % L::kLSt]);
       }
@@ -598,13 +619,16 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
       tmem_ld32(ts, reinterpret_cast<float(&)[32]>(p[0]));
       tmem_ld32(ts + 32, reinterpret_cast<float(&)[32]>(p[32]));
       tmem_ld_wait();
+      const float2 f2 = make_float2(g.scale_log2, g.scale_log2);
 #pragma unroll
-      for (int e = 0; e < 64; e += 4) {
+      for (int e = 0; e < 64; e += 4) {  // `ld` has -lse log2(e), and -D further on
         const float4 l = *reinterpret_cast<const float4*>(ld + e);
-        p[e] = exp2f(fmaf(p[e], g.scale_log2, -l.x));
-        p[e + 1] = exp2f(fmaf(p[e + 1], g.scale_log2, -l.y));
-        p[e + 2] = exp2f(fmaf(p[e + 2], g.scale_log2, -l.z));
-        p[e + 3] = exp2f(fmaf(p[e + 3], g.scale_log2, -l.w));
+        const float2 x = __ffma2_rn(make_float2(p[e], p[e + 1]), f2, make_float2(l.x, l.y));
+        const float2 y = __ffma2_rn(make_float2(p[e + 2], p[e + 3]), f2, make_float2(l.z, l.w));
+        p[e] = exp2f(x.x);
+        p[e + 1] = exp2f(x.y);
+        p[e + 2] = exp2f(y.x);
+        p[e + 3] = exp2f(y.y);
       }
       // query a + e sees key b where e >= lo, and is one of the sequence's where e < hi
       const int lo = b - off - a, hi = it.s.nq - a;
@@ -622,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&bb.p_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bb.p_full);
       ok = mbar_wait(&bb.dp_full, i & 1, err, abort_flag);
       if (!ok) break;
       tc_fence_after();
@@ -633,10 +658,15 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
 #pragma unroll
       for (int e = 0; e < 64; e += 4) {
         const float4 d = *reinterpret_cast<const float4*>(ld + 128 + e);
-        p[e] *= dp[e] - d.x;
-        p[e + 1] *= dp[e + 1] - d.y;
-        p[e + 2] *= dp[e + 2] - d.z;
-        p[e + 3] *= dp[e + 3] - d.w;
+        const float2 x = __fmul2_rn(make_float2(p[e], p[e + 1]),
+                                    __fadd2_rn(make_float2(dp[e], dp[e + 1]), make_float2(d.x, d.y)));
+        const float2 y =
+            __fmul2_rn(make_float2(p[e + 2], p[e + 3]),
+                       __fadd2_rn(make_float2(dp[e + 2], dp[e + 3]), make_float2(d.z, d.w)));
+        p[e] = x.x;
+        p[e + 1] = x.y;
+        p[e + 2] = y.x;
+        p[e + 3] = y.y;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bb.l_empty[i % L::kLSt]);
@@ -653,7 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&bb.ds_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bb.ds_full);
     }
     if (ok && n > 0) {
       ok = mbar_wait(&bb.acc_full, 0, err, abort_flag);
@@ -705,8 +736,8 @@ cudaError_t launch_causal_dvec(const CausalProblem& p, const void* o, const void
 }
 
 cudaError_t launch_causal_dq(const CausalProblem& p, const void* q, const void* k, const void* v,
-                             const ItemList& list, const void* d_o, const float* lse,
-                             const float* dvec, void* dq, int* err, cudaStream_t s) {
+                             const ItemList& list, const void* d_o, const float* lse, float* dvec,
+                             void* dq, int* err, cudaStream_t s) {
   CUtensorMap tq, tdo, tk, tv;
   if (!make_tmap_rows(&tq, q, p.total_q, p.Hq, p.d, p.q, 128) ||
       !make_tmap_rows(&tdo, d_o, p.total_q, p.Hq, p.d, p.o, 128) ||
@@ -722,8 +753,8 @@ cudaError_t launch_causal_dq(const CausalProblem& p, const void* q, const void* 
 }
 
 cudaError_t launch_causal_dkv(const CausalProblem& p, const void* q, const void* k, const void* v,
-                              const ItemList& list, const void* d_o, const float* lse,
-                              const float* dvec, void* dk, void* dv, int* err, cudaStream_t s) {
+                              const ItemList& list, const void* d_o, const float* lse, float* dvec,
+                              void* dk, void* dv, int* err, cudaStream_t s) {
   CUtensorMap tq, tdo, tk, tv;
   if (!make_tmap_rows(&tq, q, p.total_q, p.Hq, p.d, p.q, 128) ||
       !make_tmap_rows(&tdo, d_o, p.total_q, p.Hq, p.d, p.o, 128) ||

@@ -249,8 +249,8 @@ sla_status sla_causal_forward(const sla_causal_shape* shape, const void* q, cons
   int* err = at<int>(workspace, L.err);
   const SeqIn in{q_off, k_off, k_len, p.n_seq, p.total_q, p.total_k, p.max_q};
   // generated tokens: the 128-query tiles would be almost empty, and there would be too few of
-  // them (48 caches of up to 8192 keys, 16 heads over 4: 212 us with them, 81 us this way;
-  // one cache of 4001 keys, 12 heads over 4: 65 us and 8.8 us)
+  // them (48 caches of up to 8192 keys, 16 heads over 4: 212 us with them, 73 us this way;
+  // one cache of 4001 keys, 12 heads over 4: 65 us and 8.4 us)
   if ((long long)p.max_q * p.G <= kTokenRows) {
     SLA_LAUNCH("causal_token", s, launch_causal_token(p, q, k, v, in, o, lse, err, s));
     return SLA_OK;

@@ -229,12 +229,15 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_q = idesc_bf16(128, D, 0, 1);
       bool ok = mbar_wait(&bb.q_full, 0, err, abort_flag);
-      auto issue_s = [&](int h, int j) -> bool {  // S and dP
-        const int s = j % kSt;
+      // waits for tile j of K and V, before what the products of tile j - 1 wait for: a wait
+      // costs about 100 cycles also where it is over, and the tensor pipe runs dry meanwhile
+      auto have_kv = [&](int j) -> bool {
         const uint32_t ph = (j / kSt) & 1;
-        if (!mbar_wait(&bb.k_full[s], ph, err, abort_flag) ||
-            !mbar_wait(&bb.v_full[s], ph, err, abort_flag))
-          return false;
+        return mbar_wait(&bb.k_full[j % kSt], ph, err, abort_flag) &&
+               mbar_wait(&bb.v_full[j % kSt], ph, err, abort_flag);
+      };
+      auto issue_s = [&](int h, int j) {  // S and dP
+        const int s = j % kSt;
         tc_fence_after();
         const uint64_t qd = desc_kmajor_base(smem_u32(sQ + h * L::kQ)),
                        od = desc_kmajor_base(smem_u32(sDO + h * L::kQ)),
@@ -250,7 +253,6 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
           mma_commit(&bb.s_full[h]);
         }
         __syncwarp();
-        return true;
       };
       auto issue_dq = [&](int h, int j) -> bool {
         if (!mbar_wait(&bb.ds_full[h], j & 1, err, abort_flag)) return false;
@@ -266,14 +268,16 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
         __syncwarp();
         return true;
       };
+      ok = ok && have_kv(0);
       for (int h = 0; ok && h < 2; ++h)
-        if (n[h] > 0) ok = issue_s(h, 0);
+        if (n[h] > 0) issue_s(h, 0);
       if (ok && elect_sync()) mma_commit(&bb.v_empty[0]);
       __syncwarp();
       for (int j = 0; ok && j < nt; ++j) {
+        if (j + 1 < nt) ok = have_kv(j + 1);
         for (int h = 0; ok && h < 2; ++h) {
           if (j < n[h]) ok = issue_dq(h, j);
-          if (ok && j + 1 < n[h]) ok = issue_s(h, j + 1);
+          if (ok && j + 1 < n[h]) issue_s(h, j + 1);
         }
         if (ok && elect_sync()) {
           mma_commit(&bb.k_empty[j % kSt]);
@@ -524,9 +528,15 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_g = idesc_bf16(128, D, 0, 1);
       const uint64_t kd = desc_kmajor_base(smem_u32(sK)), vd = desc_kmajor_base(smem_u32(sV));
-      auto issue_s = [&](int i) -> bool {
+      // (Q and dO of step i + 1 are waited for before P and dS of step i, see the dQ kernel)
+      auto have_q = [&](int i) -> bool {
+        return mbar_wait(&bb.q_full[i % L::kQSt], (i / L::kQSt) & 1, err, abort_flag);
+      };
+      auto have_o = [&](int i) -> bool {
+        return mbar_wait(&bb.o_full[i % L::kOSt], (i / L::kOSt) & 1, err, abort_flag);
+      };
+      auto issue_s = [&](int i) {
         const int s = i % L::kQSt;
-        if (!mbar_wait(&bb.q_full[s], (i / L::kQSt) & 1, err, abort_flag)) return false;
         tc_fence_after();
         const uint64_t qd = desc_kmajor_base(smem_u32(sQ + s * L::kT));
         if (elect_sync()) {
@@ -537,11 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
           mma_commit(&bb.s_full);
         }
         __syncwarp();
-        return true;
       };
-      auto issue_dp = [&](int i) -> bool {
+      auto issue_dp = [&](int i) {
         const int s = i % L::kOSt;
-        if (!mbar_wait(&bb.o_full[s], (i / L::kOSt) & 1, err, abort_flag)) return false;
         tc_fence_after();
         const uint64_t od = desc_kmajor_base(smem_u32(sDO + s * L::kT));
         if (elect_sync()) {
@@ -552,7 +560,6 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
           mma_commit(&bb.dp_full);
         }
         __syncwarp();
-        return true;
       };
       // acc += A(TMEM) * B, A's k-step ks (16 queries) at 8 ks of the warpgroup's half
       auto issue_g = [&](uint32_t acc, uint32_t a, uint8_t* tile, int i, uint64_t* free) {
@@ -567,14 +574,21 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dkv_kernel(
         }
         __syncwarp();
       };
-      bool ok = mbar_wait(&bb.kv_full, 0, err, abort_flag) && issue_s(0) && issue_dp(0);
+      bool ok = mbar_wait(&bb.kv_full, 0, err, abort_flag) && have_q(0) && have_o(0);
+      if (ok) {
+        issue_s(0);
+        issue_dp(0);
+      }
       for (int i = 0; ok && i < n; ++i) {
-        if (!(ok = mbar_wait(&bb.p_full, i & 1, err, abort_flag))) break;
+        const bool more = i + 1 < n;
+        ok = (!more || have_q(i + 1)) && mbar_wait(&bb.p_full, i & 1, err, abort_flag);
+        if (!ok) break;
         issue_g(tmem + 256, tmem, sDO + (i % L::kOSt) * L::kT, i, &bb.o_empty[i % L::kOSt]);
-        if (i + 1 < n && !(ok = issue_s(i + 1))) break;
-        if (!(ok = mbar_wait(&bb.ds_full, i & 1, err, abort_flag))) break;
+        if (more) issue_s(i + 1);
+        ok = (!more || have_o(i + 1)) && mbar_wait(&bb.ds_full, i & 1, err, abort_flag);
+        if (!ok) break;
         issue_g(tmem + 384, tmem + 128, sQ + (i % L::kQSt) * L::kT, i, &bb.q_empty[i % L::kQSt]);
-        if (i + 1 < n) ok = issue_dp(i + 1);
+        if (more) issue_dp(i + 1);
       }
       if (elect_sync()) {
         if (ok) mma_commit(&bb.acc_full);

@@ -202,9 +202,16 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, D, 0, 1);
       bool ok = mbar_wait(&bb.q_full, 0, err, abort_flag);
-      auto issue_s = [&](int h, int j) -> bool {
+      // K and V are waited for once for both tiles, before P: a wait costs about 100 cycles also
+      // where it is over, and the tensor pipe runs dry meanwhile
+      auto have_k = [&](int j) -> bool {
+        return mbar_wait(&bb.k_full[j % kKSt], (j / kKSt) & 1, err, abort_flag);
+      };
+      auto have_v = [&](int j) -> bool {
+        return mbar_wait(&bb.v_full[j % kVSt], (j / kVSt) & 1, err, abort_flag);
+      };
+      auto issue_s = [&](int h, int j) {
         const int s = j % kKSt;
-        if (!mbar_wait(&bb.k_full[s], (j / kKSt) & 1, err, abort_flag)) return false;
         tc_fence_after();
         const uint64_t qd = desc_kmajor_base(smem_u32(sQ + h * L::kTile));
         const uint64_t kd = desc_kmajor_base(smem_u32(sK + s * L::kTile));
@@ -216,13 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
           mma_commit(&bb.s_full[h]);
         }
         __syncwarp();
-        return true;
       };
       auto issue_pv = [&](int h, int j) -> bool {
         const int s = j % kVSt;
-        if (!mbar_wait(&bb.p_full[h], j & 1, err, abort_flag) ||
-            !mbar_wait(&bb.v_full[s], (j / kVSt) & 1, err, abort_flag))
-          return false;
+        if (!mbar_wait(&bb.p_full[h], j & 1, err, abort_flag)) return false;
         tc_fence_after();
         const uint64_t vd = desc_mnmajor_base(smem_u32(sV + s * L::kTile), 128);
         if (elect_sync()) {
@@ -244,14 +248,16 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
         __syncwarp();
         return true;
       };
+      ok = ok && have_k(0);
       for (int h = 0; ok && h < 2; ++h)
-        if (n[h] > 0) ok = issue_s(h, 0);
+        if (n[h] > 0) issue_s(h, 0);
       if (ok && elect_sync()) mma_commit(&bb.k_empty[0]);
       __syncwarp();
       for (int j = 0; ok && j < nt; ++j) {
+        ok = have_v(j) && (j + 1 == nt || have_k(j + 1));
         for (int h = 0; ok && h < 2; ++h) {
           if (j < n[h]) ok = issue_pv(h, j);
-          if (ok && j + 1 < n[h]) ok = issue_s(h, j + 1);
+          if (ok && j + 1 < n[h]) issue_s(h, j + 1);
         }
         if (ok && elect_sync()) {
           mma_commit(&bb.v_empty[j % kVSt]);

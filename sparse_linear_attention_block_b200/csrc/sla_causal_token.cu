@@ -357,10 +357,12 @@ cudaError_t launch_causal_token(const CausalProblem& p, const void* q, const voi
     return cudaErrorInvalidValue;
   const int row_tiles = (p.max_q * p.G + kRows - 1) / kRows;
   const unsigned units = unsigned(p.n_seq) * p.Hkv * row_tiles;
-  // two CTAs fit on an SM: split the keys while there are fewer CTAs than that, and while a
-  // split keeps four tiles of the longest possible sequence
+  // two CTAs fit on an SM: split the keys while there are fewer CTAs than two rounds of that
+  // (sequences of uneven lengths: 48 caches of up to 8192 keys take 80 us with one round, 73 us
+  // with two, 81 us with four), and while a split keeps four tiles of the longest possible
+  // sequence
   int splits = 1;
-  while (splits < 16 && units * splits < 2 * 148 && splits * 2 * 256 <= p.total_k) splits *= 2;
+  while (splits < 16 && units * splits < 4 * 148 && splits * 2 * 256 <= p.total_k) splits *= 2;
   const CtArgs a{in,      static_cast<const __nv_bfloat16*>(q),
                  p.q.row, p.q.head,
                  static_cast<__nv_bfloat16*>(o),

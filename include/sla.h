@@ -283,8 +283,10 @@ SLA_API sla_status sla_backward_gated(const sla_shape* shape, const void* q, con
  *   - Offsets are checked on the device: a sequence whose offsets decrease or
  *     leave the tensor is skipped (nothing of it is written) and the call
  *     records SLA_ERR_DEVICE in the workspace (sla_check).
- *   - Results do not depend on the order in which CTAs run: no atomics, equal
- *     inputs give equal bits.
+ *   - Results do not depend on the order in which CTAs run: no sum is made by
+ *     atomics, equal inputs give equal bits.
+ *   - Outputs must not overlap inputs or one another, except a state that is
+ *     passed on in place where that is allowed.
  *   - The workspace is taken as with the other calls: 1024-byte aligned,
  *     sla_workspace_init() once, calls sharing it must not overlap.  It is one
  *     size for forward and backward. */
@@ -296,7 +298,8 @@ typedef struct {
  * reads key/value head h / (Hq / Hkv).  d is 64 or 128.  1 <= total_q, total_k
  * < 2^30, 1 <= n_seq <= 2^20, Hq <= 1024.
  * max_q: an upper bound of a sequence's queries, 0 for total_q.  It only picks
- * the kernel; a longer sequence is skipped and reported like a bad offset.
+ * the kernel (up to 64 rows of queries times Hq / Hkv: the one for generated
+ * tokens); a longer sequence is skipped and reported like a bad offset.
  * softmax_scale <= 0 selects 1/sqrt(d). */
 typedef struct {
   int n_seq, total_q, total_k, Hq, Hkv, d;
@@ -333,7 +336,9 @@ SLA_API sla_status sla_causal_forward(const sla_causal_shape* shape, const void*
 
 /* Gradients of sum(o * d_o) for the forward above without k_len.  o and lse are
  * the forward's; d_o has o's strides; dq, dk, dv (bf16) have those of q, k, v
- * and are overwritten at every row of a sequence (0 where nothing is seen). */
+ * and are overwritten at every row of a sequence (0 where nothing is seen).
+ * P and dS are rounded to bf16 for their products (dS to two bf16 numbers for
+ * dq); everything else is held in fp32. */
 SLA_API sla_status sla_causal_backward(const sla_causal_shape* shape, const void* q, const void* k,
                                        const void* v, const int32_t* q_off, const int32_t* k_off,
                                        const void* o, const float* lse, const void* d_o, void* dq,
@@ -362,7 +367,8 @@ SLA_API sla_status sla_decay_query_sizes(const sla_decay_shape* shape, sla_decay
  * 16-byte aligned; state_in and state_out may be the same buffer.  An empty
  * sequence passes its state on.  log_decay: fp32 [H] on the device, at most 0
  * (-inf forgets at once); a value above 0 or NaN is taken as 0 and reported as
- * SLA_ERR_DEVICE. */
+ * SLA_ERR_DEVICE.  States are held to fp32 (the increments enter with 24 bits);
+ * what a query reads of them, and q . k, is rounded to bf16. */
 SLA_API sla_status sla_decay_forward(const sla_decay_shape* shape, const void* q, const void* k,
                                      const void* v, const float* log_decay, const int32_t* off,
                                      const float* state_in, void* o, float* state_out,

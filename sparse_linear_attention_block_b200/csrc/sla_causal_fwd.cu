@@ -392,8 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
 }
 
 template <int D>
-cudaError_t launch(const CausalProblem& p, const CUtensorMap& tq, const CUtensorMap& tk,
-                   const CUtensorMap& tv, const CfArgs& a, int most, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CfArgs& a, int most, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(
       causal_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCfTotal<D>);
   if (e != cudaSuccess) return e;
@@ -422,8 +421,8 @@ cudaError_t launch_causal_fwd(const CausalProblem& p, const void* q, const void*
                  pair_heads(p),
                  p.scale_log2,
                  err};
-  return p.d == 128 ? launch<128>(p, tq, tk, tv, a, list.most, s)
-                    : launch<64>(p, tq, tk, tv, a, list.most, s);
+  return p.d == 128 ? launch<128>(tq, tk, tv, a, list.most, s)
+                    : launch<64>(tq, tk, tv, a, list.most, s);
 }
 
 }  // namespace sla

@@ -306,6 +306,66 @@ def test_captured_and_replayed_with_other_lengths():
     c.check(backward=True)
 
 
+def test_captured_tokens_replayed_with_longer_caches():
+    """A token step captured once and replayed as the caches grow."""
+    c = Case([1, 1, 1], [5, 100, 64], Hq=8, Hkv=2, d=128, cap=512, max_q=1, seed=13)
+    c.forward()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.forward()
+    for lk in ([6, 101, 65], [512, 0, 300]):
+        c.k_len.copy_(i32(lk))
+        c.seqs = [(i, 1, 512 * i, n) for i, n in enumerate(lk)]
+        c.buf.o.fill_(77.0)
+        graph.replay()
+        c.check()
+
+
+def test_streams_given_by_the_caller():
+    c = Case([200, 31], Hq=4, Hkv=2, d=64, seed=14)
+    side = torch.cuda.Stream()
+    b = c.buf
+    for stream in (side, side.cuda_stream):
+        b.o.fill_(77.0)
+        side.wait_stream(torch.cuda.current_stream())
+        slab.sla_causal_forward(c.shape, c.q, c.k, c.v, c.q_off, c.k_off, None, b.o, b.lse,
+                                b.workspace, stream=stream)
+        slab.sla_check(b.workspace, stream)
+        c.check()
+
+
+def test_shapes_follow_their_fields():
+    """A shape that is changed after a call is checked and used as it is now."""
+    c = Case([60, 20], Hq=2, Hkv=1, d=64, seed=15)
+    c.forward()
+    c.shape.softmax_scale = 0.05
+    c.scale = 0.05
+    c.forward()
+    c.check()
+    c.shape.total_q = 79
+    with pytest.raises(slab.SlaError):
+        c.forward()
+
+
+def test_a_mixed_batch_of_prompts_and_tokens():
+    """What a server runs in one call: whole prompts, a prompt that continues, generated tokens."""
+    lq, lk = [150, 1, 1, 40, 1], [150, 700, 33, 300, 1]
+    for max_q in (0, 150):
+        c = Case(lq, lk, Hq=8, Hkv=2, d=128, cap=704, max_q=max_q, seed=16)
+        c.forward()
+        c.check()
+
+
+def test_lengths_that_pass_the_work_lists_buckets():
+    """A long key range in few rows: costs of more than 2048 tiles share buckets in the list."""
+    n = 40
+    lq, lk = [70] + [3] * (n - 1), [300000] + [50] * (n - 1)
+    c = Case(lq, lk, Hq=1, Hkv=1, d=64, seed=17)
+    c.forward()
+    c.check()
+
+
 def test_two_streams_at_once():
     cases = [Case([900, 300], Hq=4, Hkv=2, d=128, seed=20 + i, backward=True) for i in range(2)]
     streams = [torch.cuda.Stream() for _ in cases]

@@ -10,12 +10,14 @@
 // needs five.  P and dS are rounded to bf16 for their products; the scores, the
 // statistics and all sums are fp32.
 // D comes from the rounded o, which would be the largest error of dq and dk after
-// their own rounding.  The dQ kernel, which runs first, feeds dS as two bf16 numbers
-// (an eighth product) and finds D's error as the sum of dS over a row (the weights
-// add up to 1); the dK/dV kernel works with the D that this gives.
-// Figures (two sequences of 8192 tokens, 12 heads over 4, d = 128): D 24 us, dQ 740
-// us, dK/dV 670 us, together 1.06 and 1.23 PFLOP/s of executed products, near the
-// power limit.  Bound for short sequences: the chain of a CTA's steps, 2500 (dQ) cycles for
+// their own rounding, and of the whole result where a row sees only a few keys.  So
+// the dQ kernel, which runs first, takes D = sum_b P_ab dP_ab from a first walk over
+// the keys where a tile sees up to 1024 of them; beyond, it feeds dS as two bf16
+// numbers (an eighth product, as after the first walk) and finds D's error as the sum
+// of dS over a row (the weights add up to 1).  The dK/dV kernel works with that D.
+// Figures (two sequences of 8192 tokens, 12 heads over 4, d = 128): D 24 us, dQ 800
+// us, dK/dV 680 us, 1.0 and 1.2 PFLOP/s of executed products, near the power limit.
+// Bound for short sequences: the chain of a CTA's steps, 2500 cycles in the dQ kernel for
 // two tiles of 64 keys.
 #include "sla_causal.h"
 #include "sla_ptx.cuh"
@@ -99,6 +101,8 @@ __device__ __forceinline__ void store_row32(uint32_t taddr, bool have, bool writ
 // with N = 64 reads 6 KB of shared memory, 48 cycles of it, for 32 of the tensor pipe
 // (measured: 48), so S and dP are bounded to 2/3 of its rate; 128 keys do not fit in TMEM for two tiles, and one tile
 // alone would double the K/V traffic from L2.
+constexpr int kExactTiles = 16;  // up to so many key tiles D is computed here
+
 template <int D>
 struct DqSmem {
   static constexpr int kQ = 128 * D * 2, kKV = 64 * D * 2;
@@ -152,6 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
   }
   const int hk = head[0] / g.G;
   const int nt = max(n[0], n[1]);
+  // steps: once over the key tiles, after a first time for D alone where they are few
+  const int passes = nt <= kExactTiles ? 2 : 1, steps = passes * nt;
 
   if (warp == 0) tmem_alloc(&bb.tmem_base, 512);
   if (threadIdx.x == 32) {
@@ -192,12 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
                         head[h]);
           }
       }
-      int nk = 0, nv = 0;
-      bool fix = false, go = true;
-      for (int j = 0; go && j < nt; ++j) {
-        const int s = j % kSt;
-        const uint32_t ph = ((j / kSt) + 1) & 1;
-        if (j >= kSt && !(go = mbar_wait(&bb.k_empty[s], ph, err, abort_flag))) break;
+      int nk = 0, nv = 0, fix = -1;  // copies issued; the last one through the fix barrier
+      bool go = true;
+      for (int i = 0; go && i < steps; ++i) {
+        const int s = i % kSt, pass = i >= nt, j = i - pass * nt;
+        const uint32_t ph = ((i / kSt) + 1) & 1;
+        if (i >= kSt && !(go = mbar_wait(&bb.k_empty[s], ph, err, abort_flag))) break;
         const int valid = it.s.nk - j * 64;
         uint8_t* dst = sK + s * L::kKV;
         uint64_t* bar = valid < 64 ? &bb.k_fix : &bb.k_full[s];
@@ -208,12 +214,12 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
         }
         ++nk;
         if (valid < 64) {  // the sequence's last keys: clear the rows behind them (0 times NaN)
-          fix = true;
-          if (!(go = mbar_wait(&bb.k_fix, 0, err, abort_flag))) break;
+          fix = i;
+          if (!(go = mbar_wait(&bb.k_fix, pass, err, abort_flag))) break;
           clear_rows<D>(dst, 64, valid);
           if (lane == 0) mbar_arrive(&bb.k_full[s]);
         }
-        if (j >= kSt && !(go = mbar_wait(&bb.v_empty[s], ph, err, abort_flag))) break;
+        if (i >= kSt && !(go = mbar_wait(&bb.v_empty[s], ph, err, abort_flag))) break;
         if (elect_sync()) {
           mbar_arrive_expect_tx(&bb.v_full[s], L::kKV);
           for (int c = 0; c < D / 64; ++c)
@@ -226,9 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
         // let copies already in flight land before the CTA exits
         mbar_wait(&bb.q_full, 0, nullptr, nullptr);
         for (int j = max(0, nk - kSt); j < nk; ++j)
-          if (!(fix && j == nk - 1))
+          if (j != fix)
             mbar_wait(&bb.k_full[j % kSt], (j / kSt) & 1, nullptr, nullptr);
-        if (fix) mbar_wait(&bb.k_fix, 0, nullptr, nullptr);
+        if (fix >= 0) mbar_wait(&bb.k_fix, fix >= nt, nullptr, nullptr);
         for (int j = max(0, nv - kSt); j < nv; ++j)
           mbar_wait(&bb.v_full[j % kSt], (j / kSt) & 1, nullptr, nullptr);
       }
@@ -236,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_q = idesc_bf16(128, D, 0, 1);
       bool ok = mbar_wait(&bb.q_full, 0, err, abort_flag);
-      // waits for tile j of K and V, before what the products of tile j - 1 wait for: a wait
+      // waits for step j's tile of K and V, before what the products of tile j - 1 wait for: a wait
       // costs about 100 cycles also where it is over, and the tensor pipe runs dry meanwhile
       auto have_kv = [&](int j) -> bool {
         const uint32_t ph = (j / kSt) & 1;
@@ -261,11 +267,12 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
         }
         __syncwarp();
       };
-      auto issue_dq = [&](int h, int j) -> bool {
-        if (!mbar_wait(&bb.ds_full[h], j & 1, err, abort_flag)) return false;
+      auto issue_dq = [&](int h, int i) -> bool {
+        const int pass = i >= nt, j = i - pass * nt;
+        if (!mbar_wait(&bb.ds_full[h], (pass * n[h] + j) & 1, err, abort_flag)) return false;
         tc_fence_after();
-        const uint64_t kd = desc_mnmajor_base(smem_u32(sK + (j % kSt) * L::kKV), 64);
-        if (elect_sync()) {
+        const uint64_t kd = desc_mnmajor_base(smem_u32(sK + (i % kSt) * L::kKV), 64);
+        if (pass == passes - 1 && elect_sync()) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)  // the high parts, then the low ones
             mma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8,
@@ -280,15 +287,17 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
         if (n[h] > 0) issue_s(h, 0);
       if (ok && elect_sync()) mma_commit(&bb.v_empty[0]);
       __syncwarp();
-      for (int j = 0; ok && j < nt; ++j) {
-        if (j + 1 < nt) ok = have_kv(j + 1);
+      for (int i = 0; ok && i < steps; ++i) {
+        const int j = i < nt ? i : i - nt, next = i + 1 == nt ? 0 : j + 1;
+        const bool more = i + 1 < steps;
+        if (more) ok = have_kv(i + 1);
         for (int h = 0; ok && h < 2; ++h) {
-          if (j < n[h]) ok = issue_dq(h, j);
-          if (ok && j + 1 < n[h]) issue_s(h, j + 1);
+          if (j < n[h]) ok = issue_dq(h, i);
+          if (ok && more && next < n[h]) issue_s(h, i + 1);
         }
         if (ok && elect_sync()) {
-          mma_commit(&bb.k_empty[j % kSt]);
-          if (j + 1 < nt) mma_commit(&bb.v_empty[(j + 1) % kSt]);
+          mma_commit(&bb.k_empty[i % kSt]);
+          if (more) mma_commit(&bb.v_empty[(i + 1) % kSt]);
         }
         __syncwarp();
       }
@@ -306,13 +315,14 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
     const int lim0 = min(it.s.nk, (h ? a0[1] : a0[0]) + off + 1);
     const size_t row = size_t(it.s.q0) + a;
     const float base = real ? g.lse[size_t(hd) * g.total_q + row] * kLog2e : 0.f;
-    const float dd = real ? g.dvec[size_t(hd) * g.total_q + row] : 0.f;
+    float dd = real && passes == 1 ? g.dvec[size_t(hd) * g.total_q + row] : 0.f;
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + h * 128, to = tmem + lane_base + 256 + h * 128;
     float2 slip = make_float2(0.f, 0.f);
     bool ok = true;
-    for (int j = 0; j < nh; ++j) {
-      ok = mbar_wait(&bb.s_full[h], j & 1, err, abort_flag);
+    for (int i = 0; i < passes * nh; ++i) {
+      const int j = i < nh ? i : i - nh;
+      ok = mbar_wait(&bb.s_full[h], i & 1, err, abort_flag);
       if (!ok) break;
       tc_fence_after();
       float sv[64], pv[64];
@@ -336,6 +346,18 @@ __global__ void __launch_bounds__(kThreads, 1) causal_dq_kernel(
         const int left = lim - j * 64;
 #pragma unroll
         for (int e = 0; e < 64; ++e) sv[e] = e < left ? sv[e] : 0.f;
+      }
+      if (i < (passes - 1) * nh) {  // D = sum_b P_ab dP_ab
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) slip = __fadd2_rn(slip, make_float2(sv[e], sv[e + 1]));
+        if (j == nh - 1) {
+          dd = slip.x + slip.y;
+          slip = make_float2(0.f, 0.f);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bb.ds_full[h]);
+        continue;
       }
       // dS as two bf16 numbers, the second 32 columns further
 #pragma unroll

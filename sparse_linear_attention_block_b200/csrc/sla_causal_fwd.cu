@@ -392,7 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1) causal_fwd_kernel(
 }
 
 template <int D>
-cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CfArgs& a, int most, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const CfArgs& a, int most, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(
       causal_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCfTotal<D>);
   if (e != cudaSuccess) return e;

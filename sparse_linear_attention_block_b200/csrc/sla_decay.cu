@@ -14,8 +14,7 @@
 namespace sla {
 namespace {
 
-// Design of a run (sm_100a).  A persistent-size CTA (one per SM, 512 threads)
-// walks a piece of a sequence in chunks of 64 tokens.  Per chunk of r tokens,
+// Design of a run (sm_100a).  A CTA (one per SM, 640 threads) walks a piece of a sequence in chunks of 64 tokens.  Per chunk of r tokens,
 // w_n = l^n, forward (reversed runs mirror the exponents):
 //   A[s][t]  = y_s . x_t                          MMA, tokens s on the lanes
 //   P[s][t]  = w_{t-s} A[s][t]  (s <= t)          bf16, to shared memory
@@ -40,8 +39,7 @@ namespace {
 //   warps 8-11   the output                                       [104]
 //   warps 12-15  the state, one row per thread, in registers      [176]
 //   warp 16      TMA copies, two chunks ahead                     [56]
-//   warp 17, 18  the products (a thread each: U and A; O1 and O2, as a barrier
-//                and a commit cost an issuing thread 60 to 250 cycles)
+//   warp 17, 18  the products (U and A; O1 and O2: their waits are not in one order)
 // TMEM: U at 0, A at 128 and 192 (two chunks), O1 256, O2 320, S (bf16) 384.
 // Figures (d = 128, 12 heads, 16384 tokens): 58 us for the run (3.5 TB/s of its
 // bytes; about 4300 cycles per chunk), 36 us for the pieces' sums, 11 us for the

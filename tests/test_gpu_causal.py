@@ -229,6 +229,28 @@ def test_many_sequences(n):
     c.check(backward=True)
 
 
+@pytest.mark.parametrize("lq", [[1, 1, 1], [2, 3, 2], [1, 2, 1, 5]], ids=str)
+def test_gradients_of_very_short_sequences(lq):
+    """Rows whose weight lies on one or two keys: the slopes nearly cancel.  A row that sees one key
+    has no slope: D and dP agree to fp32 there (d 2^-23 sum|do v| scale |k| at most), where a D
+    from the rounded output would leave 2^-9 of it."""
+    c = Case(lq, Hq=2, Hkv=1, d=64, seed=18, backward=True)
+    c.forward()
+    c.backward()
+    slab.sla_check(c.buf.workspace)
+    r, _, _, _ = ref.attention(c.q, c.k, c.v, c.seqs, c.scale, c.d_o)
+    first = [s[0] for s in c.seqs]
+    for h in range(2):
+        mass = (c.d_o[first, h].double().abs() * c.v[first, 0].double().abs()).sum(1, keepdim=True)
+        limit = 4 * 64 * 2.0 ** -23 * mass * c.scale * c.k[first, 0].double().abs()
+        assert (c.buf.dq[first, h].double().abs() <= limit + 2.0 ** -120).all()
+    # the rest as a whole: the rounding of dq itself, and of dS for dk, a root mean square of
+    # u / sqrt(3) each
+    for n, x in (("dq", c.buf.dq), ("dk", c.buf.dk)):
+        if float(r[n].norm()) > 1e-6:
+            assert float((x.double() - r[n]).norm() / r[n].norm()) <= ref.U, n
+
+
 def test_own_scale_and_max_q():
     c = Case([77, 130], Hq=2, Hkv=2, d=128, scale=0.03, max_q=130, seed=6)
     c.forward()
